@@ -367,6 +367,140 @@ int moe_route_static_status(void* stream);
 int moe_attn_seam_x8(const void* x, const void* norm_w, int M, int hidden, float eps,
                      uint8_t* x8, uint8_t* x8_codes, float* ys, void* stream);
 
+/*
+ * Residual addition, RMSNorm and MXFP8 of M bf16 token rows (device):
+ *   res_out = bf16(x + residual)
+ *   ys      = res_out * (mean(res_out^2) + eps)^(-1/2) * norm_w     (fp32)
+ *   x8, x8_codes = MXFP8 of ys (E4M3 bytes u8 [M, hidden], one E8M0 code per
+ *             32 columns u8 [M, hidden/32]), as moe_attn_seam_x8 of res_out,
+ *             bit for bit
+ *   normed  = bf16(ys) [M, hidden], if not null
+ * The norm reads the rounded sum: the row every other reader of the residual
+ * stream sees. x and residual are rows of `hidden` values ldx and ldr elements
+ * apart (multiples of 8, >= hidden); norm_w [hidden] and the outputs are
+ * contiguous. res_out may be residual or x itself where that one is
+ * contiguous; other overlaps are not allowed.
+ *
+ * One kernel on `stream` (void* holding a cudaStream_t): nothing is allocated
+ * or synchronised, capture safe. M >= 0 (0 enqueues nothing); hidden a
+ * multiple of 32 in [32, 8192]. Errors: MOE_ERR_RANGE (M), MOE_ERR_UNSUPPORTED
+ * (hidden), MOE_ERR_ARG (null, eps < 0 or NaN, a stride below hidden, in place
+ * over strided rows), MOE_ERR_ALIGN (a pointer not 16-byte aligned, a stride
+ * not a multiple of 8), MOE_ERR_CUDA. A row with NaN or infinite values is
+ * unspecified in its normed, x8 and codes; other rows are not touched by it.
+ */
+int moe_add_norm_x8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                    const void* norm_w, int M, int hidden, float eps, void* res_out, uint8_t* x8,
+                    uint8_t* x8_codes, void* normed, void* stream);
+
+/*
+ * The 8-bit paged key/value cache. A page holds MOE_KV_PAGE_TOKENS tokens;
+ * per page, key/value head and kind (0 keys, 1 values) it keeps 64 * head_dim
+ * E4M3 bytes and one E8M0 code: byte b under code c stands for
+ * e4m3(b) * 2^(c - 127).
+ *  blocks  u8 [pages, kv_heads, 2, 64 * head_dim] (device, 16-byte aligned)
+ *  codes   u8 [pages, kv_heads, 2]                (device)
+ * Byte of (token t, dim d) in a page's images (the shared-memory images the
+ * attention kernel's matrix loads read):
+ *  keys    t * D + 16 * ((d / 16) ^ s) + d % 16, s = t % 8 (D = 128, 256) or
+ *          (t / 2) % 4 (D = 64)
+ *  values  d * 64 + 16 * ((t / 16) ^ ((d / 2) % 4)) + 4 * ((t % 8) / 2)
+ *          + 2 * ((t % 16) / 8) + t % 2
+ * head_dim is 64, 128 or 256; kv_heads 1..1024. The caller owns both arrays;
+ * a page needs no initial value.
+ */
+#define MOE_KV_PAGE_TOKENS 64
+typedef struct moe_kv_cache {
+  uint8_t* blocks;
+  uint8_t* codes;
+  int pages;
+  int kv_heads;
+  int head_dim;
+} moe_kv_cache;
+
+/*
+ * The sequences of one call (device arrays of int32, read by the kernels).
+ *  page_table [seqs, max_pages]  page of a sequence's tokens 64 i .. 64 i + 63
+ *  lens       [seqs]             tokens of each sequence: for the append, those
+ *                                already in the cache; for the attention, those
+ *                                in the cache with the query tokens' own
+ *  cu_q       [seqs + 1]         first row of each sequence's tokens among the
+ *                                call's, ascending from 0 to `tokens`; or null:
+ *                                one token each (tokens == seqs)
+ *  tokens                        rows of the call (0 enqueues nothing)
+ *  max_q                         (attention, with cu_q) the largest number of
+ *                                tokens of one sequence: a kernel is chosen by
+ *                                it, results do not depend on it
+ */
+typedef struct moe_kv_seqs {
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* cu_q;
+  int seqs;
+  int tokens;
+  int max_pages;
+  int max_q;
+} moe_kv_seqs;
+
+/* Bits of the cache kernels' status word (an int32 on the device that the
+ * caller owns and clears; null: not wanted). A bad entry is skipped, nothing
+ * is read or written out of range. */
+#define MOE_KV_STATUS_TIMEOUT 1 /* a bounded wait expired: outputs unspecified, clear the workspace */
+#define MOE_KV_STATUS_PAGE 2    /* a page id outside [0, pages): its tokens are left out */
+#define MOE_KV_STATUS_LENGTH 4  /* a length below 0 or beyond the page table: clamped / not written */
+
+/*
+ * Appends new keys and values: row r of k and v (bf16, kv_heads x head_dim
+ * contiguous values, rows ldk / ldv elements apart) is the next token of its
+ * sequence, the i-th new one going to position lens[b] + i. Per page, head and
+ * kind the code becomes
+ *   max(the code of the page's earlier tokens (none: 0), the seam's code of
+ *       the new values' largest finite magnitude),
+ * the new bytes are E4M3 round-to-nearest-even of x * 2^(127 - code), and
+ * where the code grew the earlier tokens' bytes are rounded again under it
+ * (powers of two: a byte moves exactly outside E4M3's subnormals). Infinite
+ * values are stored as +-448 under the code, NaN as NaN; neither changes the
+ * scale. Bytes of the page's later tokens are unspecified. Appending the same
+ * tokens again at the same positions changes nothing; appending others there
+ * (drafted tokens replaced) keeps the larger scale.
+ *
+ * One kernel on `stream`; no allocation, no synchronisation, capture safe.
+ * Two sequences of a call must not share a page they append to. Errors:
+ * MOE_ERR_ARG, MOE_ERR_RANGE (negative or > 2^20 sequences, 2^24 tokens),
+ * MOE_ERR_UNSUPPORTED (head_dim, kv_heads), MOE_ERR_ALIGN (k, v or blocks not
+ * 16-byte aligned, strides not multiples of 8), MOE_ERR_CUDA.
+ */
+int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* k,
+                     int64_t ldk, const void* v, int64_t ldv, int32_t* status, void* stream);
+
+/*
+ * Attention of query rows over the cache. Row i of the n rows of a sequence
+ * with kv = lens[b] tokens sits at position pos = kv - n + i and sees the
+ * tokens j <= pos with window == 0, j > pos - window or j < sinks (a sliding
+ * window that keeps the first tokens visible). q_heads is a multiple of
+ * kv_heads; query head h reads key/value head h / (q_heads / kv_heads).
+ *   out = softmax(scale * q . k) v  bf16 [tokens, q_heads, head_dim]
+ *   lse = ln sum exp(scale * q . k) f32  [tokens, q_heads], if not null
+ * A row that sees nothing gives 0 and -infinity. q bf16 [tokens, q_heads *
+ * head_dim], rows ldq elements apart. Masked tokens never touch a row, whatever
+ * their bytes (unwritten pages may hold NaN); a row whose q is not finite is
+ * unspecified and touches no other. Results do not change from run to run.
+ *
+ * workspace: device memory (16-byte aligned) of at least
+ * MOE_ATTN_X8_WORKSPACE_BYTES (enough for every call), zero before its first
+ * use; each call leaves it ready for the next. Calls that may overlap on the
+ * GPU need workspaces of their own. One kernel on `stream`; no allocation, no
+ * synchronisation, capture safe. Only pages that some row sees are read.
+ * Errors as moe_kv_append_x8, and MOE_ERR_ARG for a scale that is not positive
+ * and finite, a negative window or sinks, max_q < 1, q_heads not a multiple of
+ * kv_heads, or a workspace that is too small; MOE_ERR_UNSUPPORTED for more
+ * than 256 query heads per key/value head.
+ */
+#define MOE_ATTN_X8_WORKSPACE_BYTES (48u << 20)
+int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* q, int64_t ldq,
+                int q_heads, float scale, int window, int sinks, void* out, float* lse,
+                void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,6 +47,23 @@ class MoeDebug(ctypes.Structure):
                 ("normed", "x8", "x8_codes", "topk_ids", "topk_w", "logits")]
 
 
+# the 8-bit key/value cache
+KV_PAGE_TOKENS = 64
+KV_STATUS_TIMEOUT, KV_STATUS_PAGE, KV_STATUS_LENGTH = 1, 2, 4
+ATTN_X8_WORKSPACE_BYTES = 48 << 20
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("seqs", ctypes.c_int), ("tokens", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int)]
+
+
 _LIB = None
 
 
@@ -89,6 +106,15 @@ def lib() -> ctypes.CDLL:
     L.moe_destroy.restype = None
     L.moe_attn_seam_x8.argtypes = [vp, vp, ip, ip, ctypes.c_float, vp, vp, vp, vp]
     L.moe_attn_seam_x8.restype = ip
+    i64, fp = ctypes.c_int64, ctypes.c_float
+    L.moe_add_norm_x8.argtypes = [vp, i64, vp, i64, vp, ip, ip, fp, vp, vp, vp, vp, vp]
+    L.moe_add_norm_x8.restype = ip
+    L.moe_kv_append_x8.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), vp, i64, vp,
+                                   i64, vp, vp]
+    L.moe_kv_append_x8.restype = ip
+    L.moe_attn_x8.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), vp, i64, ip, fp, ip,
+                              ip, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    L.moe_attn_x8.restype = ip
     L.moe_test_withhold_ready.argtypes = [vp, ip]
     L.moe_test_withhold_ready.restype = ip
     L.moe_route_static.argtypes = [vp, vp, vp, ip, ip, ip, ip, vp, vp, vp]

@@ -1,0 +1,213 @@
+"""The attention side of a decode layer, on torch tensors: residual addition +
+RMSNorm + MXFP8, the 8-bit paged key/value cache, and the attention over it.
+
+Argument marshalling only, like :mod:`.api`: tensor shapes, dtypes, devices and
+strides are checked here (the kernels' loads are unbounded), the work runs in
+the library's CUDA kernels on the current stream. Nothing synchronises: what
+the kernels find in device data (page ids, lengths) is reported in the bits of
+an int32 ``status`` tensor if one is passed (``KV_STATUS_*`` of :mod:`._lib`).
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _lib
+from ._lib import ATTN_X8_WORKSPACE_BYTES, KV_PAGE_TOKENS, KvCache, KvSeqs, check
+
+
+def _rows(name: str, t: torch.Tensor, shape: tuple, device) -> int:
+    """Checks bf16 rows of contiguous values (any row stride); returns the stride."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be bf16 {shape} on {device}, got {t.dtype} {tuple(t.shape)} {t.device}")
+    width = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and st != width and t.shape[0] > 0:
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+        width *= n
+    return t.stride(0) if t.shape[0] > 1 else width  # (one row or none: any stride)
+
+
+def _dense(name: str, t, shape: tuple, dtype, device) -> None:
+    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} {t.device}")
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(device) -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def add_norm_x8(x: torch.Tensor, residual: torch.Tensor, norm_w: torch.Tensor, eps: float = 1e-6,
+                res_out: torch.Tensor | None = None, x8: torch.Tensor | None = None,
+                codes: torch.Tensor | None = None, normed: torch.Tensor | None = None):
+    """res_out = bf16(x + residual), its RMSNorm with ``norm_w``, and the norm's
+    MXFP8 (``moe_add_norm_x8``) for rows [M, H], M any.
+
+    x and residual: bf16 [M, H], rows may be strided. Returns (res_out bf16
+    [M, H], x8 uint8 [M, H], codes uint8 [M, H/32], normed): outputs not passed
+    are allocated here, except ``normed`` (the norm in bf16), which is written
+    only if a tensor is passed. ``res_out`` may be ``residual`` (or ``x``) itself
+    if that is contiguous.
+    """
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a CUDA bf16 [M, H] tensor")
+    M, H = x.shape
+    dev = x.device
+    if H % 32:
+        raise ValueError("H must be a multiple of 32")
+    ldx = _rows("x", x, (M, H), dev)
+    ldr = _rows("residual", residual, (M, H), dev)
+    _dense("norm_w", norm_w, (H,), torch.bfloat16, dev)
+    _dense("res_out", res_out, (M, H), torch.bfloat16, dev)
+    _dense("x8", x8, (M, H), torch.uint8, dev)
+    _dense("codes", codes, (M, H // 32), torch.uint8, dev)
+    _dense("normed", normed, (M, H), torch.bfloat16, dev)
+    with torch.cuda.device(dev):
+        if res_out is None:
+            res_out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        if x8 is None:
+            x8 = torch.empty((M, H), dtype=torch.uint8, device=dev)
+        if codes is None:
+            codes = torch.empty((M, H // 32), dtype=torch.uint8, device=dev)
+        check(_lib.lib().moe_add_norm_x8(
+            x.data_ptr(), ldx, residual.data_ptr(), ldr, norm_w.data_ptr(), M, H, float(eps),
+            res_out.data_ptr(), x8.data_ptr(), codes.data_ptr(), _ptr(normed), _stream(dev)),
+            "moe_add_norm_x8")
+    return res_out, x8, codes, normed
+
+
+# ---------------------------------------------------------------- the cache
+def kv_cache_x8(pages: int, kv_heads: int, head_dim: int, device="cuda"):
+    """(blocks uint8 [pages, kv_heads, 2, 64 * head_dim], codes uint8 [pages,
+    kv_heads, 2]) of an empty cache; a page needs no initial value."""
+    blocks = torch.empty((pages, kv_heads, 2, KV_PAGE_TOKENS * head_dim), dtype=torch.uint8, device=device)
+    codes = torch.zeros((pages, kv_heads, 2), dtype=torch.uint8, device=device)
+    return blocks, codes
+
+
+def kv_dequant_x8(blocks: torch.Tensor, codes: torch.Tensor) -> torch.Tensor:
+    """The values the cache stands for, fp32 [pages, kv_heads, 2, 64, head_dim]
+    (for tests and inspection: torch indexing, any device)."""
+    pages, heads, _, size = blocks.shape
+    d = size // KV_PAGE_TOKENS
+    t = torch.arange(KV_PAGE_TOKENS, device=blocks.device)[:, None]
+    c = torch.arange(d, device=blocks.device)[None, :]
+    s = t % 8 if d >= 128 else t // 2 % 4
+    key = t * d + 16 * ((c // 16) ^ s) + c % 16
+    value = c * KV_PAGE_TOKENS + 16 * ((t // 16) ^ (c // 2 % 4)) + 4 * (t % 8 // 2) + 2 * (t % 16 // 8) + t % 2
+    index = torch.stack((key, value)).reshape(2, -1)
+    byte = torch.gather(blocks, 3, index.expand(pages, heads, 2, size))
+    scale = torch.exp2(codes.double() - 127).float()
+    return (byte.view(torch.float8_e4m3fn).float() * scale[..., None]).view(pages, heads, 2, KV_PAGE_TOKENS, d)
+
+
+def _cache(blocks: torch.Tensor, codes: torch.Tensor):
+    if blocks.dim() != 4 or not blocks.is_cuda or blocks.dtype != torch.uint8 or blocks.shape[2] != 2 \
+            or not blocks.is_contiguous() or blocks.shape[3] % KV_PAGE_TOKENS:
+        raise ValueError("blocks must be a contiguous CUDA uint8 [pages, kv_heads, 2, 64 * head_dim] tensor")
+    pages, heads, _, size = blocks.shape
+    _dense("codes", codes, (pages, heads, 2), torch.uint8, blocks.device)
+    return KvCache(blocks.data_ptr(), codes.data_ptr(), pages, heads, size // KV_PAGE_TOKENS)
+
+
+def _seqs(page_table, lens, cu_q, tokens: int, max_q: int, device):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [seqs, max_pages] tensor")
+    n = page_table.shape[0]
+    _dense("page_table", page_table, tuple(page_table.shape), torch.int32, device)
+    _dense("lens", lens, (n,), torch.int32, device)
+    if cu_q is None:
+        if tokens != n:
+            raise ValueError(f"{tokens} rows for {n} sequences: without cu_q each has one")
+    else:
+        _dense("cu_q", cu_q, (n + 1,), torch.int32, device)
+    return KvSeqs(page_table.data_ptr(), lens.data_ptr(), _ptr(cu_q), n, tokens, page_table.shape[1],
+                  max_q)
+
+
+def kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                 page_table: torch.Tensor, start: torch.Tensor, cu_q: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None):
+    """Writes new keys and values into the cache (``moe_kv_append_x8``).
+
+    k, v: bf16 [tokens, kv_heads, head_dim], rows may be strided (parts of a
+    projection's output). page_table int32 [seqs, max_pages], start int32 [seqs]
+    (tokens each sequence has already), cu_q int32 [seqs + 1] (rows of each
+    sequence; None: one each). Changes blocks and codes in place and returns them.
+    """
+    cache = _cache(blocks, codes)
+    dev = blocks.device
+    if k.dim() != 3:
+        raise ValueError("k must be a bf16 [tokens, kv_heads, head_dim] tensor")
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    ldk, ldv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
+    seqs = _seqs(page_table, start, cu_q, k.shape[0], 1, dev)
+    _dense("status", status, (1,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        check(_lib.lib().moe_kv_append_x8(ctypes.byref(cache), ctypes.byref(seqs), k.data_ptr(), ldk,
+                                          v.data_ptr(), ldv, _ptr(status), _stream(dev)),
+              "moe_kv_append_x8")
+    return blocks, codes
+
+
+def attn_x8_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for :func:`attn_x8` (zeroed; enough for every call)."""
+    return torch.zeros(ATTN_X8_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def attn_x8(q: torch.Tensor, blocks: torch.Tensor, codes: torch.Tensor, page_table: torch.Tensor,
+            kv_len: torch.Tensor, cu_q: torch.Tensor | None = None, max_q: int | None = None,
+            scale: float | None = None, window: int = 0, sinks: int = 0,
+            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Attention of query rows over the cache (``moe_attn_x8``).
+
+    q: bf16 [tokens, q_heads, head_dim], rows may be strided; row i of a
+    sequence's n sits at position kv_len - n + i and sees the tokens up to it,
+    with ``window`` > 0 only the last ``window`` of them and the first ``sinks``
+    tokens. kv_len int32 [seqs] counts the tokens in the cache, the query
+    tokens' own included; cu_q as in :func:`kv_append_x8`. max_q: the largest
+    number of rows of one sequence, by which the kernel is chosen (default: all
+    of them). scale defaults to head_dim ** -0.5.
+
+    Returns (out bf16 [tokens, q_heads, head_dim], lse): ``lse`` (float32
+    [tokens, q_heads]) is written only if a tensor is passed. A program that
+    calls this often keeps a ``workspace`` (:func:`attn_x8_workspace`), one for
+    each stream; without one, a zeroed one is allocated for the call.
+    """
+    cache = _cache(blocks, codes)
+    dev = blocks.device
+    if q.dim() != 3:
+        raise ValueError("q must be a bf16 [tokens, q_heads, head_dim] tensor")
+    tokens, heads, d = q.shape
+    ldq = _rows("q", q, (tokens, heads, cache.head_dim), dev)
+    if cu_q is None:
+        max_q = 1
+    elif max_q is None:
+        max_q = max(tokens, 1)
+    seqs = _seqs(page_table, kv_len, cu_q, tokens, max_q, dev)
+    _dense("out", out, (tokens, heads, d), torch.bfloat16, dev)
+    _dense("lse", lse, (tokens, heads), torch.float32, dev)
+    _dense("status", status, (1,), torch.int32, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = attn_x8_workspace(dev)
+        check(_lib.lib().moe_attn_x8(
+            ctypes.byref(cache), ctypes.byref(seqs), q.data_ptr(), ldq, heads,
+            1.0 / math.sqrt(d) if scale is None else float(scale), int(window), int(sinks),
+            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _ptr(status), _stream(dev)), "moe_attn_x8")
+    return out, lse

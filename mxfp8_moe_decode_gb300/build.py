@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_decode.so")
 SOURCES = ["api.cu", "seam.cu", "router.cu", "scales.cu", "expert.cu", "combine.cu",
-           "route_static.cu", "attn_seam.cu"]
+           "route_static.cu", "attn_seam.cu", "add_norm.cu", "kv_append.cu", "attn_x8.cu",
+           "attn_x8_d64.cu", "attn_x8_d128.cu", "attn_x8_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -1,0 +1,97 @@
+// Host side of the cache attention: argument checks, the choice of the kernel
+// variant, and the workspace's layout (tickets, then two partial blocks per
+// CTA).
+#include <cmath>
+
+#include "internal.cuh"
+#include "kv_x8.cuh"
+
+namespace moe {
+
+// Rows of a row group for `rows` query rows of one sequence and key/value
+// head: one tile of 8 per warp, two while one warp per page still keeps up
+// with HBM, then pages shared by 4 or 8 warps of two tiles each.
+int attn_x8_group_rows(int head_dim, int rows) {
+  if (rows <= 8) return 8;
+  if (head_dim == 256) return 32;
+  return rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+}
+
+namespace {
+
+constexpr size_t kTicketBytes = 4096;
+constexpr int kMaxGrid = static_cast<int>(kTicketBytes / sizeof(int));
+
+bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
+
+size_t workspace_bytes(int grid, int head_dim, int rows) {
+  return kTicketBytes + static_cast<size_t>(grid) * 2 * attn_x8_group_rows(head_dim, rows) *
+                            (head_dim + 2) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* q,
+                           int64_t ldq, int q_heads, float scale, int window, int sinks, void* out,
+                           float* lse, void* workspace, size_t workspace_size, int32_t* status,
+                           void* stream) {
+  using namespace moe;
+  const int rc = kv_check(cache, seqs);
+  if (rc != MOE_OK) return rc;
+  if (q_heads < 1 || q_heads % cache->kv_heads) return MOE_ERR_ARG;
+  const int group = q_heads / cache->kv_heads;
+  if (group > 256) return MOE_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || std::isinf(scale) || window < 0 || sinks < 0) return MOE_ERR_ARG;
+  if (seqs->max_q < 1) return MOE_ERR_ARG;
+  if (seqs->tokens == 0) return MOE_OK;
+  if (!q || !out || !workspace) return MOE_ERR_ARG;
+  if (!aligned(q, 16) || ldq % 8 || !aligned(out, 16) || !aligned(workspace, 16) ||
+      (lse && !aligned(lse, 4)) || (status && !aligned(status, 4)))
+    return MOE_ERR_ALIGN;
+  if (ldq < static_cast<int64_t>(q_heads) * cache->head_dim) return MOE_ERR_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  const int max_q = seqs->cu_q ? (seqs->max_q < seqs->tokens ? seqs->max_q : seqs->tokens) : 1;
+  const int rows = max_q > (1 << 20) / group ? 1 << 20 : max_q * group;
+  if (workspace_size < workspace_bytes(grid, cache->head_dim, rows)) return MOE_ERR_ARG;
+  AttnX8Params p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.ldq = ldq;
+  p.blocks = cache->blocks;
+  p.codes = cache->codes;
+  p.page_table = seqs->page_table;
+  p.kv_len = seqs->lens;
+  p.cu_q = seqs->cu_q;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.tickets = static_cast<int*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTicketBytes);
+  p.status = status;
+  p.tokens = seqs->tokens;
+  p.seqs = seqs->seqs;
+  p.max_pages = seqs->max_pages;
+  p.pages = cache->pages;
+  p.kv_heads = cache->kv_heads;
+  p.group = group;
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (cache->head_dim) {
+    case 64: e = launch_attn_x8_d64(p, rows, grid, st); break;
+    case 128: e = launch_attn_x8_d128(p, rows, grid, st); break;
+    default: e = launch_attn_x8_d256(p, rows, grid, st); break;
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}

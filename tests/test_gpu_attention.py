@@ -1,0 +1,466 @@
+"""The attention side's kernels against the float64 oracle.
+
+Bounds (half a step of bf16, with its 8 significant bits, is 2^-8 of the value, of f16 2^-11):
+* add_norm: the sum bit for bit; the norm as tests/test_gpu_attn_seam.py (1e-5
+  of the row's largest value) plus bf16's rounding; bytes and codes bit for
+  bit those of the attention seam's kernel on the summed rows.
+* append: bytes and codes bit for bit (scales are powers of two).
+* attention, per value: 2^-8 |out| (the output's rounding) + (2^-11 + 2 slack)
+  * sum_j w_j |v_j| (the weights' f16 rounding, and scores off by at most
+  `slack`: 2 D fp32 roundings of the product and the part of q below what the
+  two E4M3 parts hold) + 2^-20 sum w |v| (fp32 sums of a page, exp2's two units
+  and the joins). lse: slack + (n / 8 + 64) 2^-24 + 2^-22 (1 + |lse|).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_moe_decode_gb300 as M
+from mxfp8_moe_decode_gb300 import _lib
+from oracle import attention as A
+from oracle import moe as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+PAGE = 64
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ---------------------------------------------------------------- add + norm
+def _norm_case(m, h, seed=0, pad_x=0, pad_r=0):
+    g = torch.Generator().manual_seed(seed + 7 * m + h)
+    x = torch.randn(m, h + pad_x, generator=g).bfloat16().to(DEV)[:, :h]
+    r = (3 * torch.randn(m, h + pad_r, generator=g)).bfloat16().to(DEV)[:, :h]
+    w = (1 + 0.1 * torch.randn(h, generator=g)).bfloat16().to(DEV)
+    return x, r, w
+
+
+def _check_norm(x, r, w, eps=1e-6, **kw):
+    normed = torch.empty(x.shape, dtype=torch.bfloat16, device=DEV)
+    res, x8, codes, n = M.add_norm_x8(x, r, w, eps, normed=normed, **kw)
+    torch.cuda.synchronize()
+    assert n is normed
+    want = A.add(f64(x), f64(r))
+    assert np.array_equal(f64(res), want)
+    ys = O.attn_norm(want, f64(w), eps)
+    top = np.abs(ys).max(-1, keepdims=True)
+    assert (np.abs(f64(normed) - ys) <= 1e-5 * top + 2.0 ** -8 * np.abs(ys)).all()
+    for lo in range(0, x.shape[0], 48):
+        s8, sc, _ = M.attn_seam_x8(res[lo:lo + 48].contiguous(), w, eps)
+        assert torch.equal(x8[lo:lo + 48], s8) and torch.equal(codes[lo:lo + 48], sc)
+    return res, x8, codes
+
+
+@pytest.mark.parametrize("h", [32, 96, 1024, 1056, 5120, 8192])
+@pytest.mark.parametrize("m", [1, 3, 48, 131])
+def test_add_norm(m, h):
+    _check_norm(*_norm_case(m, h))
+
+
+def test_add_norm_strided_rows_and_in_place():
+    x, r, w = _norm_case(19, 1056, pad_x=8, pad_r=64)
+    a = _check_norm(x, r, w)
+    r2 = r.contiguous().clone()
+    res, x8, codes, normed = M.add_norm_x8(x, r2, w, res_out=r2)
+    assert res is r2 and normed is None
+    assert torch.equal(res, a[0]) and torch.equal(x8, a[1]) and torch.equal(codes, a[2])
+
+
+def test_add_norm_rows_apart():
+    """A row of NaN or infinity leaves the others alone; no rows are fine."""
+    x, r, w = _norm_case(9, 512)
+    a = M.add_norm_x8(x, r, w)
+    x2 = x.clone()
+    x2[3, 5], x2[6, 100] = float("nan"), float("inf")
+    b = M.add_norm_x8(x2, r, w)
+    keep = [0, 1, 2, 4, 5, 7, 8]
+    for p, q in zip(a[:3], b[:3]):
+        assert torch.equal(p[keep], q[keep])
+    e = M.add_norm_x8(x[:0], r[:0], w)
+    assert e[0].shape == (0, 512) and e[2].shape == (0, 16)
+
+
+def test_add_norm_many_rows():
+    x, r, w = _norm_case(70000, 32)
+    res, x8, codes, _ = M.add_norm_x8(x, r, w)
+    part = M.add_norm_x8(x[69000:], r[69000:], w)
+    assert torch.equal(res[69000:], part[0]) and torch.equal(x8[69000:], part[1])
+    assert torch.equal(codes[69000:], part[2])
+
+
+# ---------------------------------------------------------------- the cache
+class Cache:
+    """A pool, page tables in shuffled order, and the same on the host."""
+
+    def __init__(self, lens, kvh, d, seed=0, spare=2, extra_width=0):
+        rng = np.random.default_rng(seed)
+        self.rng = rng
+        need = [-(-n // PAGE) for n in lens]
+        self.pages = sum(need) + spare
+        order = rng.permutation(self.pages)
+        width = max(max(need, default=1), 1) + extra_width
+        self.table = rng.integers(-3, self.pages + 3, (len(lens), width)).astype(np.int32)  # junk past the ends
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.blocks = np.full((self.pages, kvh, 2, PAGE * d), 0x7F, dtype=np.uint8)
+        self.codes = rng.integers(0, 256, (self.pages, kvh, 2)).astype(np.uint8)
+        self.lens, self.kvh, self.d = list(lens), kvh, d
+
+    def fill(self, amp=1.0):
+        """Written tokens of every sequence; the rest of the pool stays NaN."""
+        k = (amp * self.rng.standard_normal((sum(self.lens), self.kvh, self.d)) *
+             np.exp(self.rng.standard_normal((1, self.kvh, 1))))
+        v = self.rng.standard_normal((sum(self.lens), self.kvh, self.d))
+        cu = np.concatenate(([0], np.cumsum(self.lens))).tolist()
+        self.blocks, self.codes = A.append(self.blocks, self.codes, A.bf16_rne(k), A.bf16_rne(v), self.table,
+                                           [0] * len(self.lens), cu)
+        return self
+
+    def gpu(self):
+        return (torch.from_numpy(self.blocks).to(DEV), torch.from_numpy(self.codes).to(DEV),
+                torch.from_numpy(self.table).to(DEV))
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _append_case(had, new, kvh, d, seed=0, cu=True, amp=None):
+    c = Cache([a + b for a, b in zip(had, new)], kvh, d, seed)
+    lens, c.lens = c.lens, list(had)
+    c.fill()
+    c.lens = lens
+    cu_q = np.concatenate(([0], np.cumsum(new))).tolist()
+    t = cu_q[-1]
+    x = c.rng.standard_normal((t, 2, kvh, d))
+    if amp is not None:
+        x = x * amp[:t, None, None, None]
+    x = torch.from_numpy(x).bfloat16().to(DEV)
+    blocks, codes, table = c.gpu()
+    status = i32([0])
+    M.kv_append_x8(blocks, codes, x[:, 0], x[:, 1], table, i32(had), cu_q=i32(cu_q) if cu else None, status=status)
+    want = A.append(c.blocks, c.codes, f64(x[:, 0]), f64(x[:, 1]), c.table, had, cu_q)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    got = blocks.cpu().numpy()
+    # bytes of later tokens of a touched page are unspecified: compare what the sequences hold
+    held = np.zeros((c.pages, PAGE), dtype=bool)
+    for b, n in enumerate(c.lens):
+        for j in range(n):
+            held[c.table[b, j // PAGE], j % PAGE] = True
+    untouched = np.ones(c.pages, dtype=bool)
+    for b, n in enumerate(new):
+        for p in range(had[b] // PAGE, -(-(had[b] + n) // PAGE) if n else 0):
+            untouched[c.table[b, p]] = False
+    assert np.array_equal(got[untouched], c.blocks[untouched])
+    for kind, image in enumerate(A.image_bytes(d)):
+        a, w = got[:, :, kind][..., image], want[0][:, :, kind][..., image]
+        h = np.broadcast_to(held[:, None, :, None], a.shape)
+        nan = (a & 0x7F == 0x7F) & (w & 0x7F == 0x7F)
+        assert ((a == w) | nan | ~h).all()
+    assert np.array_equal(codes.cpu().numpy(), want[1])
+    return blocks, codes, table, x, cu_q
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("had,new", [
+    ([0], [1]), ([63], [1]), ([64], [1]), ([5], [0]), ([0, 17, 64, 100], [1, 1, 1, 1]),
+    ([0, 60, 3], [64, 8, 9]), ([1, 63, 0, 30, 127], [200, 2, 130, 0, 65]), ([50], [300]),
+])
+def test_append(had, new, d):
+    _append_case(had, new, 3, d, seed=d + len(had))
+    if all(n == 1 for n in new):
+        _append_case(had, new, 2, d, seed=d, cu=False)
+
+
+def test_append_scales_grow_and_stay():
+    """Loud new tokens move a page's earlier bytes, quiet ones do not (also by
+    more than E4M3's range, where they vanish)."""
+    for amp in (2.0 ** 3, 2.0 ** 8, 2.0 ** 30, 2.0 ** 90, 2.0 ** -20, 2.0 ** -110, 0.0):
+        _append_case([40, 7], [9, 1], 2, 128, amp=np.full(10, amp))
+
+
+def test_append_keeps_non_finite_values_apart():
+    amp = np.ones(70)
+    amp[3], amp[20], amp[69] = np.nan, np.inf, -np.inf
+    _append_case([10], [70], 1, 64, amp=amp)
+
+
+def test_append_many_sequences():
+    rng = np.random.default_rng(3)
+    had = rng.integers(0, 130, 300).tolist()
+    _append_case(had, rng.integers(0, 3, 300).tolist(), 1, 64)
+
+
+def test_append_again_changes_nothing_and_strides():
+    blocks, codes, table, x, cu_q = _append_case([30], [50], 2, 128)
+    b0, c0 = blocks.clone(), codes.clone()
+    wide = torch.zeros(50, 3, 2, 128, dtype=torch.bfloat16, device=DEV)
+    wide[:, 1], wide[:, 2] = x[:, 0], x[:, 1]
+    M.kv_append_x8(blocks, codes, wide[:, 1], wide[:, 2], table, i32([30]), cu_q=i32(cu_q))
+    assert torch.equal(codes, c0)
+    val = M.kv_dequant_x8(blocks, codes)[table[0, :2].long()]
+    was = M.kv_dequant_x8(b0, c0)[table[0, :2].long()]
+    tok = torch.arange(128, device=DEV).view(2, 1, 1, 64, 1) < 80
+    assert torch.equal(torch.where(tok, val, 0), torch.where(tok, was, 0))
+
+
+def test_append_reports_bad_pages_and_lengths():
+    """Page ids out of range, lengths below 0 or past the table: skipped and
+    reported, nothing else is written."""
+    c = Cache([10, 10, 10, 64], 2, 64).fill()
+    k = torch.ones(4, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for table, start, bit in [((0, -1), 0, _lib.KV_STATUS_PAGE), ((0, c.pages), 0, _lib.KV_STATUS_PAGE),
+                              (None, -5, _lib.KV_STATUS_LENGTH), (None, 64, _lib.KV_STATUS_LENGTH)]:
+        t = c.table.copy()
+        start0 = [10, 10, 10, 63]
+        if table:
+            t[0, 0] = table[1]
+            t[1:3, 0] = -1
+            t[3, 0] = c.pages + 100
+        else:
+            start0 = [start] * 4
+        blocks, codes, _ = c.gpu()
+        status = i32([0])
+        M.kv_append_x8(blocks, codes, k, k, torch.from_numpy(t).to(DEV), i32(start0), status=status)
+        torch.cuda.synchronize()
+        assert status.item() == bit
+        assert np.array_equal(blocks.cpu().numpy(), c.blocks) and np.array_equal(codes.cpu().numpy(), c.codes)
+
+
+# ---------------------------------------------------------------- the attention
+def _check_attn(c, n, heads, window=0, sinks=0, cu=True, q=None, max_q=None, lens=None, scale=None, ws=None):
+    lens = c.lens if lens is None else lens
+    cu_q = np.concatenate(([0], np.cumsum(n))).tolist()
+    t = cu_q[-1]
+    if q is None:
+        q = torch.from_numpy(2 * c.rng.standard_normal((t, heads, c.d))).bfloat16().to(DEV)
+    blocks, codes, table = c.gpu()
+    lse = torch.full((t, heads), 7.0, device=DEV)
+    status = i32([0])
+    ws = M.attn_x8_workspace(DEV) if ws is None else ws
+    args = dict(cu_q=i32(cu_q) if cu else None, max_q=max(max(n), 1) if max_q is None else max_q, scale=scale,
+                window=window, sinks=sinks, workspace=ws, status=status)
+    out, got_lse = M.attn_x8(q, blocks, codes, table, i32(lens), lse=lse, **args)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and got_lse is lse
+    s = c.d ** -0.5 if scale is None else scale
+    want, wl, spread, slack = A.attention(f64(q), A.cache_values(c.blocks, c.codes), c.table, lens, cu_q, s,
+                                          window, sinks)
+    got, gl = f64(out), f64(lse)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) - bound).max())
+    empty = np.isinf(wl)
+    assert np.array_equal(np.isinf(gl), empty) and (gl[empty] < 0).all() and (got[empty] == 0).all()
+    tol = slack + (max(lens) / 8 + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(wl))
+    assert (np.abs(gl[~empty] - wl[~empty]) <= tol[~empty]).all()
+    again, _ = M.attn_x8(q, blocks, codes, table, i32(lens), **args)  # and the same bits again
+    assert torch.equal(again, out)
+    return out, lse
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kvh,group", [(1, 1), (2, 5), (3, 8), (1, 16), (2, 13)])
+def test_attention_single_tokens(kvh, group, d):
+    c = Cache([1, 64, 65, 7, 200, 128], kvh, d, seed=group).fill()
+    _check_attn(c, [1] * 6, kvh * group, cu=False)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,lens", [
+    ([3, 0, 8, 1], [70, 64, 8, 500]),   # a sequence without rows, one that is all query rows
+    ([5, 2], [3, 0]),                   # more rows than tokens: rows that see nothing
+    ([48], [190]), ([20, 1, 7], [64, 129, 63]),
+])
+@pytest.mark.parametrize("group", [1, 5, 8])
+def test_attention_several_tokens(n, lens, group, d):
+    c = Cache(lens, 2, d, seed=d + group).fill()
+    _check_attn(c, n, 2 * group)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (64, 0), (65, 1), (100, 64), (7, 130), (1000, 5), (130, 0)])
+@pytest.mark.parametrize("n", [[1, 1, 1], [6, 3, 9]])
+def test_attention_window_and_sinks(window, sinks, n):
+    c = Cache([640, 130, 65], 2, 128, seed=window).fill()
+    _check_attn(c, n, 10, window, sinks)
+    _check_attn(c, n, 2, window, sinks)
+
+
+def test_attention_one_long_sequence_over_all_ctas():
+    c = Cache([20000], 1, 64, seed=5).fill()
+    ws = M.attn_x8_workspace(DEV)
+    for _ in range(2):  # the workspace is ready again after each call
+        _check_attn(c, [1], 5, cu=False, ws=ws)
+    assert not ws[:4096].any()
+
+
+def test_attention_many_short_sequences():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 90, 600).tolist()
+    c = Cache(lens, 1, 64).fill()
+    _check_attn(c, [1] * 600, 3, cu=False)
+
+
+def test_attention_variants_agree():
+    """max_q only picks the kernel: one row, two tiles, shared pages."""
+    c = Cache([700, 90], 2, 128, seed=9).fill()
+    q = torch.from_numpy(c.rng.standard_normal((2, 6, 128))).bfloat16().to(DEV)
+    for max_q in (1, 4, 20, 40):
+        _check_attn(c, [1, 1], 6, q=q, max_q=max_q)
+
+
+@pytest.mark.parametrize("amp,qamp", [(40.0, 1.0), (1.0, 2.0 ** 60), (2.0 ** -60, 1.0), (1.0, 0.0)])
+def test_attention_peaked_flat_and_far_scales(amp, qamp):
+    """Scores of hundreds, rows of large, tiny and zero values."""
+    c = Cache([300, 64], 2, 128, seed=1).fill(amp)
+    q = torch.from_numpy(qamp * c.rng.standard_normal((2, 4, 128))).bfloat16().to(DEV)
+    _check_attn(c, [1, 1], 4, q=q, scale=128 ** -0.5 / max(qamp, 1.0))
+
+
+def test_attention_long_tail_is_kept():
+    """One token 2^-17 times heavier than each of 6000 others: the others still
+    hold their share (8-bit weights would lose it)."""
+    c = Cache([6001], 1, 64, seed=2)
+    k = np.zeros((6001, 1, 64))
+    k[0, 0, 0] = 448.0
+    v = np.ones((6001, 1, 64))
+    v[0] = -1.0
+    c.blocks, c.codes = A.append(c.blocks, c.codes, k, v, c.table, [0], [0, 6001])
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device=DEV)
+    q[0, 0, 0] = 1.0
+    _check_attn(c, [1], 1, cu=False, q=q, scale=17 * np.log(2) / 448)
+
+
+def test_attention_nan_stays_where_it_is_masked():
+    """A NaN token is seen by the rows after it only, also on the same page and
+    in the same tile of rows; one outside the window by none."""
+    c = Cache([200], 1, 128, seed=4).fill()
+    blocks, codes, table = c.gpu()
+    q = torch.from_numpy(c.rng.standard_normal((6, 3, 128))).bfloat16().to(DEV)
+    key, value = A.image_bytes(128)
+    clean, _ = M.attn_x8(q, blocks, codes, table, i32([200]), cu_q=i32([0, 6]), max_q=6)
+    page = c.table[0, 197 // 64]
+    for kind, image in ((0, key), (1, value)):
+        b = blocks.clone()
+        b[page, 0, kind, torch.from_numpy(image[197 % 64]).to(DEV)] = 0x7F
+        out, _ = M.attn_x8(q, b, codes, table, i32([200]), cu_q=i32([0, 6]), max_q=6)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:3], clean[:3])  # rows 194, 195, 196
+        assert torch.isnan(out[3:]).all()
+    clean, _ = M.attn_x8(q, blocks, codes, table, i32([200]), cu_q=i32([0, 6]), max_q=6, window=20, sinks=2)
+    b = blocks.clone()
+    for t in (2, 100, 174):
+        for kind, image in ((0, key), (1, value)):
+            b[c.table[0, t // 64], 0, kind, torch.from_numpy(image[t % 64]).to(DEV)] = 0x7F
+    out, _ = M.attn_x8(q, b, codes, table, i32([200]), cu_q=i32([0, 6]), max_q=6, window=20, sinks=2)
+    assert torch.equal(out, clean)
+
+
+def test_attention_row_of_nan_queries_touches_no_other():
+    c = Cache([100, 100], 1, 128, seed=6).fill()
+    q = torch.from_numpy(c.rng.standard_normal((2, 4, 128))).bfloat16().to(DEV)
+    blocks, codes, table = c.gpu()
+    a, _ = M.attn_x8(q, blocks, codes, table, i32([100, 100]))
+    q2 = q.clone()
+    q2[0, 1, 3], q2[1, 2, 0] = float("nan"), float("inf")
+    b, _ = M.attn_x8(q2, blocks, codes, table, i32([100, 100]))
+    a, b = a.clone(), b.clone()
+    for t in (a, b):
+        t[0, 1] = 0
+        t[1, 2] = 0
+    assert torch.equal(a, b)
+
+
+def test_attention_strided_queries_and_other_stream():
+    c = Cache([150, 33], 2, 64, seed=8).fill()
+    wide = torch.from_numpy(c.rng.standard_normal((2, 10, 64))).bfloat16().to(DEV)
+    q = wide[:, :6]
+    a, _ = _check_attn(c, [1, 1], 6, q=q)
+    blocks, codes, table = c.gpu()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b, _ = M.attn_x8(q, blocks, codes, table, i32([150, 33]), cu_q=i32([0, 1, 2]), max_q=1)
+    s.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_attention_reports_bad_pages_and_lengths():
+    c = Cache([200, 70], 1, 64, seed=3).fill()
+    q = torch.from_numpy(c.rng.standard_normal((2, 2, 64))).bfloat16().to(DEV)
+    blocks, codes, _ = c.gpu()
+    ws = M.attn_x8_workspace(DEV)
+
+    def call(table, lens):
+        status = i32([0])
+        out, _ = M.attn_x8(q, blocks, codes, torch.from_numpy(table).to(DEV), i32(lens), workspace=ws, status=status)
+        torch.cuda.synchronize()
+        return out, status.item()
+
+    good, st = call(c.table, [200, 70])
+    assert st == 0
+    for bad in (-1, c.pages, 1 << 30):
+        t = c.table.copy()
+        t[0, 1] = bad
+        out, st = call(t, [200, 70])
+        assert st == _lib.KV_STATUS_PAGE and torch.equal(out[1], good[1]) and torch.isfinite(out).all()
+    width = c.table.shape[1] * 64
+    out, st = call(c.table, [-4, 70])
+    assert st == _lib.KV_STATUS_LENGTH and (out[0] == 0).all() and torch.equal(out[1], good[1])
+    full = Cache([width, 70], 1, 64, seed=3).fill()
+    blocks, codes, _ = full.gpu()
+    good, st = call(full.table, [width, 70])
+    out, st2 = call(full.table, [width + 5, 70])
+    assert (st, st2) == (0, _lib.KV_STATUS_LENGTH) and torch.equal(out, good)
+
+
+def test_append_then_attention_in_a_graph():
+    """A decode step captured once and replayed as the sequences grow."""
+    d, kvh, heads = 128, 2, 10
+    c = Cache([130, 64], kvh, d, seed=11, extra_width=1).fill()
+    c.table[1, 1] = [p for p in range(c.pages) if p not in set(c.table[0, :3]) | {c.table[1, 0]}][0]
+    blocks, codes, table = c.gpu()
+    start, lens = i32([130, 64]), i32([131, 65])
+    x = torch.zeros(2, 2, kvh, d, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(2, heads, d, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    ws = M.attn_x8_workspace(DEV)
+
+    def step():
+        M.kv_append_x8(blocks, codes, x[:, 0], x[:, 1], table, start)
+        M.attn_x8(q, blocks, codes, table, lens, out=out, workspace=ws)
+        start.add_(1)
+        lens.add_(1)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    keep = [t.clone() for t in (blocks, codes, start, lens)]
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    for t, k in zip((blocks, codes, start, lens), keep):
+        t.copy_(k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    hb, hc = c.blocks, c.codes
+    for i in range(3):
+        xn = torch.from_numpy(c.rng.standard_normal(tuple(x.shape)) * 4 ** i).bfloat16()
+        qn = torch.from_numpy(c.rng.standard_normal(tuple(q.shape))).bfloat16()
+        x.copy_(xn)
+        q.copy_(qn)
+        graph.replay()
+        torch.cuda.synchronize()
+        at = [130 + i, 64 + i]
+        hb, hc = A.append(hb, hc, f64(xn)[:, 0], f64(xn)[:, 1], c.table, at, [0, 1, 2])
+        want, _, spread, slack = A.attention(f64(qn), A.cache_values(hb, hc), c.table, [a + 1 for a in at],
+                                             [0, 1, 2], d ** -0.5)
+        bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread
+        assert (np.abs(f64(out) - want) <= bound).all()
