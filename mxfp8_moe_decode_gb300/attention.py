@@ -10,7 +10,6 @@ an int32 ``status`` tensor if one is passed (``KV_STATUS_*`` of :mod:`._lib`).
 
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
@@ -21,29 +20,43 @@ from ._lib import ATTN_X8_WORKSPACE_BYTES, KV_PAGE_TOKENS, KvCache, KvSeqs, chec
 
 def _rows(name: str, t: torch.Tensor, shape: tuple, device) -> int:
     """Checks bf16 rows of contiguous values (any row stride); returns the stride."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be bf16 {shape} on {device}, got {t.dtype} {tuple(t.shape)} {t.device}")
-    width = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and st != width and t.shape[0] > 0:
-            raise ValueError(f"{name}: the values of a row must be contiguous")
-        width *= n
-    return t.stride(0) if t.shape[0] > 1 else width  # (one row or none: any stride)
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be bf16 {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} {t.device}")
+    stride = t.stride()
+    if len(shape) == 3:
+        width = shape[1] * shape[2]
+        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
+    else:
+        width = shape[1]
+        dense = stride[1] == 1 or width == 1
+    if not dense and shape[0] > 0:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return stride[0] if shape[0] > 1 else width  # (one row or none: any stride)
 
 
 def _dense(name: str, t, shape: tuple, dtype, device) -> None:
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or t.device != device
-                          or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on {device}, "
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} {t.device}")
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+# The decode step's calls are a few microseconds of GPU work each, so the way to
+# the launch is kept short: torch's own accessors behind current_device() and
+# current_stream(), without their argument handling.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _call(name: str, fn, index: int, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    if _current_device() == index:
+        code = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        check(code, name)
 
 
 def add_norm_x8(x: torch.Tensor, residual: torch.Tensor, norm_w: torch.Tensor, eps: float = 1e-6,
@@ -60,28 +73,31 @@ def add_norm_x8(x: torch.Tensor, residual: torch.Tensor, norm_w: torch.Tensor, e
     """
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError("x must be a CUDA bf16 [M, H] tensor")
-    M, H = x.shape
+    shape = x.shape
+    M, H = shape
     dev = x.device
     if H % 32:
         raise ValueError("H must be a multiple of 32")
-    ldx = _rows("x", x, (M, H), dev)
-    ldr = _rows("residual", residual, (M, H), dev)
+    ldx = _rows("x", x, shape, dev)
+    ldr = _rows("residual", residual, shape, dev)
     _dense("norm_w", norm_w, (H,), torch.bfloat16, dev)
-    _dense("res_out", res_out, (M, H), torch.bfloat16, dev)
-    _dense("x8", x8, (M, H), torch.uint8, dev)
-    _dense("codes", codes, (M, H // 32), torch.uint8, dev)
-    _dense("normed", normed, (M, H), torch.bfloat16, dev)
-    with torch.cuda.device(dev):
-        if res_out is None:
-            res_out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
-        if x8 is None:
-            x8 = torch.empty((M, H), dtype=torch.uint8, device=dev)
-        if codes is None:
-            codes = torch.empty((M, H // 32), dtype=torch.uint8, device=dev)
-        check(_lib.lib().moe_add_norm_x8(
-            x.data_ptr(), ldx, residual.data_ptr(), ldr, norm_w.data_ptr(), M, H, float(eps),
-            res_out.data_ptr(), x8.data_ptr(), codes.data_ptr(), _ptr(normed), _stream(dev)),
-            "moe_add_norm_x8")
+    if res_out is None:
+        res_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _dense("res_out", res_out, shape, torch.bfloat16, dev)
+    if x8 is None:
+        x8 = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _dense("x8", x8, shape, torch.uint8, dev)
+    if codes is None:
+        codes = torch.empty((M, H // 32), dtype=torch.uint8, device=dev)
+    else:
+        _dense("codes", codes, (M, H // 32), torch.uint8, dev)
+    if normed is not None:
+        _dense("normed", normed, shape, torch.bfloat16, dev)
+    _call("moe_add_norm_x8", _lib.lib().moe_add_norm_x8, dev.index, x.data_ptr(), ldx,
+          residual.data_ptr(), ldr, norm_w.data_ptr(), M, H, eps, res_out.data_ptr(), x8.data_ptr(),
+          codes.data_ptr(), None if normed is None else normed.data_ptr())
     return res_out, x8, codes, normed
 
 
@@ -111,8 +127,8 @@ def kv_dequant_x8(blocks: torch.Tensor, codes: torch.Tensor) -> torch.Tensor:
 
 
 def _cache(blocks: torch.Tensor, codes: torch.Tensor):
-    if blocks.dim() != 4 or not blocks.is_cuda or blocks.dtype != torch.uint8 or blocks.shape[2] != 2 \
-            or not blocks.is_contiguous() or blocks.shape[3] % KV_PAGE_TOKENS:
+    if blocks.dim() != 4 or not blocks.is_cuda or blocks.dtype != torch.uint8 or not blocks.is_contiguous() \
+            or blocks.shape[2] != 2 or blocks.shape[3] % KV_PAGE_TOKENS:
         raise ValueError("blocks must be a contiguous CUDA uint8 [pages, kv_heads, 2, 64 * head_dim] tensor")
     pages, heads, _, size = blocks.shape
     _dense("codes", codes, (pages, heads, 2), torch.uint8, blocks.device)
@@ -122,16 +138,22 @@ def _cache(blocks: torch.Tensor, codes: torch.Tensor):
 def _seqs(page_table, lens, cu_q, tokens: int, max_q: int, device):
     if page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [seqs, max_pages] tensor")
-    n = page_table.shape[0]
-    _dense("page_table", page_table, tuple(page_table.shape), torch.int32, device)
+    n, width = page_table.shape
+    _dense("page_table", page_table, (n, width), torch.int32, device)
     _dense("lens", lens, (n,), torch.int32, device)
     if cu_q is None:
         if tokens != n:
             raise ValueError(f"{tokens} rows for {n} sequences: without cu_q each has one")
-    else:
-        _dense("cu_q", cu_q, (n + 1,), torch.int32, device)
-    return KvSeqs(page_table.data_ptr(), lens.data_ptr(), _ptr(cu_q), n, tokens, page_table.shape[1],
-                  max_q)
+        return KvSeqs(page_table.data_ptr(), lens.data_ptr(), None, n, tokens, width, max_q)
+    _dense("cu_q", cu_q, (n + 1,), torch.int32, device)
+    return KvSeqs(page_table.data_ptr(), lens.data_ptr(), cu_q.data_ptr(), n, tokens, width, max_q)
+
+
+def _status(status, device):
+    if status is None:
+        return None
+    _dense("status", status, (1,), torch.int32, device)
+    return status.data_ptr()
 
 
 def kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -151,11 +173,9 @@ def kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, k: torch.Tensor, v: 
     shape = (k.shape[0], cache.kv_heads, cache.head_dim)
     ldk, ldv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
     seqs = _seqs(page_table, start, cu_q, k.shape[0], 1, dev)
-    _dense("status", status, (1,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        check(_lib.lib().moe_kv_append_x8(ctypes.byref(cache), ctypes.byref(seqs), k.data_ptr(), ldk,
-                                          v.data_ptr(), ldv, _ptr(status), _stream(dev)),
-              "moe_kv_append_x8")
+    st = _status(status, dev)
+    _call("moe_kv_append_x8", _lib.lib().moe_kv_append_x8, dev.index, cache, seqs, k.data_ptr(), ldk,
+          v.data_ptr(), ldv, st)
     return blocks, codes
 
 
@@ -195,19 +215,19 @@ def attn_x8(q: torch.Tensor, blocks: torch.Tensor, codes: torch.Tensor, page_tab
     elif max_q is None:
         max_q = max(tokens, 1)
     seqs = _seqs(page_table, kv_len, cu_q, tokens, max_q, dev)
-    _dense("out", out, (tokens, heads, d), torch.bfloat16, dev)
-    _dense("lse", lse, (tokens, heads), torch.float32, dev)
-    _dense("status", status, (1,), torch.int32, dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+    st = _status(status, dev)
+    if out is None:
+        out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _dense("out", out, (tokens, heads, d), torch.bfloat16, dev)
+    if lse is not None:
+        _dense("lse", lse, (tokens, heads), torch.float32, dev)
+    if workspace is None:
+        workspace = attn_x8_workspace(dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            workspace = attn_x8_workspace(dev)
-        check(_lib.lib().moe_attn_x8(
-            ctypes.byref(cache), ctypes.byref(seqs), q.data_ptr(), ldq, heads,
-            1.0 / math.sqrt(d) if scale is None else float(scale), int(window), int(sinks),
-            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _ptr(status), _stream(dev)), "moe_attn_x8")
+    _call("moe_attn_x8", _lib.lib().moe_attn_x8, dev.index, cache, seqs, q.data_ptr(), ldq, heads,
+          1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), st)
     return out, lse

@@ -10,11 +10,11 @@ namespace moe {
 
 // Rows of a row group for `rows` query rows of one sequence and key/value
 // head: one tile of 8 per warp, two while one warp per page still keeps up
-// with HBM, then pages shared by 4 or 8 warps of two tiles each.
+// with HBM, then pages shared by 3 or 6 warps of two tiles each.
 int attn_x8_group_rows(int head_dim, int rows) {
   if (rows <= 8) return 8;
-  if (head_dim == 256) return 32;
-  return rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+  if (head_dim == 256) return 24;
+  return rows <= 16 ? 16 : rows <= 48 ? 48 : 96;
 }
 
 namespace {
@@ -59,6 +59,12 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
   const int max_q = seqs->cu_q ? (seqs->max_q < seqs->tokens ? seqs->max_q : seqs->tokens) : 1;
   const int rows = max_q > (1 << 20) / group ? 1 << 20 : max_q * group;
+  // rows and the list of pages are counted in 32 bits, whatever the lengths on the device
+  if (static_cast<long long>(seqs->tokens) * group * group > UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const long long groups =
+      static_cast<long long>(seqs->tokens) * group / attn_x8_group_rows(cache->head_dim, rows) + seqs->seqs;
+  if (groups * cache->kv_heads > INT32_MAX / (seqs->max_pages + 8ll))
+    return MOE_ERR_UNSUPPORTED;
   if (workspace_size < workspace_bytes(grid, cache->head_dim, rows)) return MOE_ERR_ARG;
   AttnX8Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -79,15 +85,17 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   p.pages = cache->pages;
   p.kv_heads = cache->kv_heads;
   p.group = group;
+  p.group_magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(group) + 1);
+  p.max_kv = seqs->max_pages * kPageTokens;
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (cache->head_dim) {
-    case 64: e = launch_attn_x8_d64(p, rows, grid, st); break;
-    case 128: e = launch_attn_x8_d128(p, rows, grid, st); break;
-    default: e = launch_attn_x8_d256(p, rows, grid, st); break;
+    case 64: e = launch_attn_x8_d64(p, rows, dev, grid, st); break;
+    case 128: e = launch_attn_x8_d128(p, rows, dev, grid, st); break;
+    default: e = launch_attn_x8_d256(p, rows, dev, grid, st); break;
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

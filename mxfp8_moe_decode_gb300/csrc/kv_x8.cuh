@@ -105,15 +105,20 @@ struct AttnX8Params {
   int* tickets;            // workspace: [grid] CTAs of a shared item that are done (0 between calls)
   int* status;             // or null
   int tokens, seqs, max_pages, pages, kv_heads, group;
+  unsigned group_magic;    // floor(2^32 / group) + 1 (unused for a group of 1)
+  int max_kv;              // 64 * max_pages, the longest a sequence can be
   int window, sinks;
   float scale_log2;        // scale * log2(e)
 };
 
 // one instantiation per head dim (their own translation units); `rows`: the
 // largest number of query rows of one sequence and key/value head
-cudaError_t launch_attn_x8_d64(const AttnX8Params& p, int rows, int grid, cudaStream_t s);
-cudaError_t launch_attn_x8_d128(const AttnX8Params& p, int rows, int grid, cudaStream_t s);
-cudaError_t launch_attn_x8_d256(const AttnX8Params& p, int rows, int grid, cudaStream_t s);
+cudaError_t launch_attn_x8_d64(const AttnX8Params& p, int rows, int device, int grid,
+                               cudaStream_t s);
+cudaError_t launch_attn_x8_d128(const AttnX8Params& p, int rows, int device, int grid,
+                               cudaStream_t s);
+cudaError_t launch_attn_x8_d256(const AttnX8Params& p, int rows, int device, int grid,
+                               cudaStream_t s);
 // rows of one row group for that many query rows
 int attn_x8_group_rows(int head_dim, int rows);
 
