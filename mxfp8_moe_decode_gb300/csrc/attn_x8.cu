@@ -1,6 +1,6 @@
 // Host side of the cache attention: argument checks, the choice of the kernel
-// variant, and the workspace's layout (tickets, then two partial blocks per
-// CTA).
+// variant, and the workspace's layout (tickets, records, then two partial
+// blocks per CTA).
 #include <cmath>
 
 #include "internal.cuh"
@@ -10,22 +10,24 @@ namespace moe {
 
 // Rows of a row group for `rows` query rows of one sequence and key/value
 // head: one tile of 8 per warp, two while one warp per page still keeps up
-// with HBM, then pages shared by 3 or 6 warps of two tiles each.
+// with HBM; beyond, the tcgen05 kernel's two tiles of 128, or (D = 256, whose
+// key rows are not an operand tile) pages shared by three warps.
 int attn_x8_group_rows(int head_dim, int rows) {
   if (rows <= 8) return 8;
   if (head_dim == 256) return 24;
-  return rows <= 16 ? 16 : rows <= 48 ? 48 : 96;
+  return rows <= 16 ? 16 : 256;
 }
 
 namespace {
 
-constexpr size_t kTicketBytes = 4096;
-constexpr int kMaxGrid = static_cast<int>(kTicketBytes / sizeof(int));
+constexpr int kMaxGrid = 384;
+constexpr size_t kTicketBytes = 4096;               // 4 bytes a CTA
+constexpr size_t kHeadBytes = kTicketBytes + 12288;  // and 32 bytes a CTA of records
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
 
 size_t workspace_bytes(int grid, int head_dim, int rows) {
-  return kTicketBytes + static_cast<size_t>(grid) * 2 * attn_x8_group_rows(head_dim, rows) *
+  return kHeadBytes + static_cast<size_t>(grid) * 2 * attn_x8_group_rows(head_dim, rows) *
                             (head_dim + 2) * sizeof(float);
 }
 
@@ -77,7 +79,8 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.tickets = static_cast<int*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTicketBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeadBytes);
+  p.records = static_cast<uint8_t*>(workspace) + kTicketBytes;
   p.status = status;
   p.tokens = seqs->tokens;
   p.seqs = seqs->seqs;

@@ -125,6 +125,38 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// One lane of a converged warp. (A branch on it, unlike one on the lane number,
+// tells the compiler that a single thread issues what follows; the instructions
+// that take uniform operands -- tcgen05, bulk copies -- otherwise cost it a
+// loop over the lanes each.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// Bounded wait for an mbarrier phase: about a second of SM clocks, or until the
+// CTA's abort flag is set (which a wait that runs out does). The clock is the
+// SM's own: a read of %globaltimer on the way costs about as much as the whole
+// wait for a product.
+constexpr long long kWaitClocks = 2000000000ll;
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kWaitClocks) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- work list
 // A CTA's start and end are chains of scalar code that nothing overlaps, so
 // the divisions in them are short ones.
@@ -215,6 +247,101 @@ __device__ __forceinline__ bool next_segment(const AttnX8Params& p, Walk& k) {
   return false;
 }
 
+// This CTA's run of the work list, found by every warp for itself, 32 sequences
+// at a time (nothing to wait for but the lengths): once over them for the
+// list's length, once more to the run's start. False: nothing to do (the same
+// in every warp). `teams`: pages that a CTA works on at once. parts: CTAs per
+// item (aligned runs), or 0 and then per: list positions per run.
+template <int kRows>
+__device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int lane, int warp, Walk& walk,
+                                         int& per, int& parts) {
+  parts = 0;
+  int total = 0, items = 0, longest = 0;
+  bool odd_len = false;
+  for (int b = lane; b < p.seqs; b += 32) {
+    const Seq s = load_seq<kRows>(p, b);
+    odd_len |= __ldg(p.kv_len + b) != s.kv;
+    const int n = s.groups * p.kv_heads;
+    total += item_size(s) * n;
+    items += n;
+    longest = max(longest, s.pages);
+  }
+  if (odd_len && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, kKvErrLength);
+  total = __reduce_add_sync(0xffffffffu, total);
+  items = __reduce_add_sync(0xffffffffu, items);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (items == 0) return false;
+  const int cta = blockIdx.x, grid = gridDim.x;
+  per = div_pos(total + grid - 1, grid);
+  // Aligned: every item in `parts` equal parts, when that makes no run much
+  // longer than an equal share, each part at least two pages per team
+  // (shorter ones save less than the join costs).
+  if (items <= grid) {
+    const int k = max(min(div_pos(grid, items), longest / (2 * teams)), 1);
+    if (div_pos(longest + k - 1, k) <= max(per + per / 8, 2 * teams)) parts = k;
+  }
+  // list: no run shorter than one page per team while items have as many
+  if (parts == 0) per = max(per, min(teams, div_pos(total, items)));
+  const int at = parts ? div_pos(cta, parts) : min(per * cta, total);  // item, or list position
+  if (at >= (parts ? items : total)) return false;
+  int base = 0, seen = 0;  // list position and units before the current 32 sequences
+  for (int b0 = 0;; b0 += 32) {
+    Seq s = {};
+    if (b0 + lane < p.seqs) s = load_seq<kRows>(p, b0 + lane);
+    const int n = s.groups * p.kv_heads, size = item_size(s) * n, step = parts ? n : size;
+    const int all = __reduce_add_sync(0xffffffffu, step);
+    if (at >= seen + all && b0 + 32 < p.seqs) {
+      seen += all;
+      base += __reduce_add_sync(0xffffffffu, size);
+      continue;
+    }
+    int upto = step, pos = size;  // inclusive sums over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o), v = __shfl_up_sync(0xffffffffu, pos, o);
+      if (lane >= o) {
+        upto += u;
+        pos += v;
+      }
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, at < seen + upto)) - 1;  // (there is one)
+    walk.b = b0 + who;
+    walk.base = base + __shfl_sync(0xffffffffu, pos - size, who);
+    seen += __shfl_sync(0xffffffffu, upto - step, who);
+    walk.s.q0 = __shfl_sync(0xffffffffu, s.q0, who);
+    walk.s.n = __shfl_sync(0xffffffffu, s.n, who);
+    walk.s.kv = __shfl_sync(0xffffffffu, s.kv, who);
+    walk.s.sink_pages = __shfl_sync(0xffffffffu, s.sink_pages, who);
+    walk.s.lo = __shfl_sync(0xffffffffu, s.lo, who);
+    walk.s.pages = __shfl_sync(0xffffffffu, s.pages, who);
+    walk.s.groups = __shfl_sync(0xffffffffu, s.groups, who);
+    break;
+  }
+  if (parts) {
+    const int len = div_pos(walk.s.pages + parts - 1, parts);
+    const int first = (cta - at * parts) * len;
+    if (first >= walk.s.pages) return false;
+    walk.w = walk.base + (at - seen) * item_size(walk.s) + kItemCost + first;
+    walk.end = walk.w + min(len, walk.s.pages - first);
+  } else {
+    walk.w = at;
+    walk.end = min(at + per, total);
+  }
+  return true;
+}
+
+// The first and last CTA of an item of which this CTA has a part.
+__device__ __forceinline__ void item_ctas(int item_start, int pages, int per, int parts, int& c0, int& c1) {
+  if (parts) {
+    c0 = div_pos(blockIdx.x, parts) * parts;
+    const int len = div_pos(pages + parts - 1, parts);
+    c1 = c0 + div_pos(pages + len - 1, len) - 1;
+  } else {
+    c0 = div_pos(item_start + kItemCost, per);
+    c1 = div_pos(item_start + kItemCost + pages - 1, per);
+  }
+}
+
 // A segment whose item other CTAs share, joined at the CTA's end.
 struct Shared {
   int c0, c1;  // the item's CTAs (c1 < 0: no such segment)
@@ -222,6 +349,107 @@ struct Shared {
   int last;    // this CTA arrived last
   int pad;
 };
+
+// Does a row at position `at` see a token?
+__device__ __forceinline__ bool sees(const AttnX8Params& p, int token, int at) {
+  return token <= at && (p.window == 0 || token > at - p.window || token < p.sinks);
+}
+
+// What rows at positions lo .. hi see of tokens t0 .. t1: 0 nothing, 1 all of
+// it every one, 2 otherwise.
+__device__ __forceinline__ int page_kind(const AttnX8Params& p, int t0, int t1, int lo, int hi) {
+  if (t1 <= lo && (p.window == 0 || t0 > hi - p.window || t1 < p.sinks)) return 1;
+  if (t0 > hi || (p.window > 0 && t1 <= lo - p.window && t0 >= p.sinks)) return 0;
+  return 2;
+}
+
+// Four dims of a finished row: sum / den, and with the first ones the lse;
+// sum and den are held times 2^log2_scale relative to `top` (log2 units).
+template <int D>
+__device__ __forceinline__ void store_row(const AttnX8Params& p, int q0, int head, int r, int d4, const float4& sum,
+                                          float top, float den, float log2_scale) {
+  const int token = by_group(p, r);
+  const size_t at = static_cast<size_t>(q0 + token) * (p.kv_heads * p.group) + head * p.group + r - token * p.group;
+  const float inv = den == 0.0f ? 0.0f : __frcp_rn(den);
+  __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(sum.x * inv, sum.y * inv),
+                                      __floats2bfloat162_rn(sum.z * inv, sum.w * inv)};
+  *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
+  if (d4 == 0 && p.lse)
+    p.lse[at] = den == 0.0f ? -INFINITY : (top + log2f(den) - log2_scale) * 0.69314718055994531f;
+}
+
+// Four dims of a row of a shared item, from its parts in CTA order. A part holds
+// its rows' sums, row by row or (kCols) four dims of all rows after another,
+// and then each row's {m, l}.
+template <int D, int kRows, bool kCols = false>
+__device__ __forceinline__ void join_row(const AttnX8Params& p, const Shared& x, int lr, int d4, float log2_scale) {
+  const auto partial = [&](int c) {
+    return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
+  };
+  float top = -INFINITY, den = 0.0f;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int cb = x.c0; cb <= x.c1; cb += 8) {  // eight parts' loads in flight
+    float4 y[8];
+    float2 t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* src = partial(min(cb + k, x.c1));
+      y[k] = __ldcg(reinterpret_cast<const float4*>(src) + (kCols ? d4 * kRows + lr : lr * (D / 4) + d4));
+      t[k] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + lr);
+    }
+    float high = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) high = fmaxf(high, t[k].x);
+    const float use = high == -INFINITY ? 0.0f : high;
+    const float keep = ex2(top - use);
+    top = high;
+    den *= keep;
+    sum.x *= keep;
+    sum.y *= keep;
+    sum.z *= keep;
+    sum.w *= keep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (cb + k > x.c1) break;
+      const float w = ex2(t[k].x - use);
+      den = fmaf(t[k].y, w, den);
+      sum.x = fmaf(y[k].x, w, sum.x);
+      sum.y = fmaf(y[k].y, w, sum.y);
+      sum.z = fmaf(y[k].z, w, sum.z);
+      sum.w = fmaf(y[k].w, w, sum.w);
+    }
+  }
+  store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, log2_scale);
+}
+
+// The CTA's end: items of several CTAs (a run has at most two). The last CTA
+// to arrive joins their partial rows. All threads call this after a barrier
+// behind their partial rows.
+template <int D, int kRows>
+__device__ __forceinline__ void join_shared(const AttnX8Params& p, Shared* shared, int tid, int threads,
+                                            float log2_scale) {
+  if (shared[0].c1 < 0 && shared[1].c1 < 0) return;  // (the same in every thread)
+  if (tid == 0) {
+    __threadfence();
+    for (int i = 0; i < 2; ++i) {
+      Shared& x = shared[i];
+      x.last = 0;
+      if (x.c1 < 0) continue;
+      if (atomicAdd(p.tickets + x.c0, 1) == x.c1 - x.c0) {
+        p.tickets[x.c0] = 0;
+        x.last = 1;
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  for (int i = 0; i < 2; ++i) {
+    const Shared x = shared[i];
+    if (x.c1 < 0 || !x.last) continue;
+    const int count = min(kRows, x.rows - x.row0) * (D / 4);
+    for (int u = tid; u < count; u += threads) join_row<D, kRows>(p, x, u / (D / 4), u % (D / 4), log2_scale);
+  }
+}
 
 // ---------------------------------------------------------------- the kernel
 template <int D, int NT, int RW>
@@ -255,84 +483,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  // ---- this CTA's run. Every warp goes over the sequences by itself, 32 at a
-  // time (nothing to wait for but the lengths): once for the list's length,
-  // once more to the run's start.
+  // ---- this CTA's run
   Walk walk;
-  int per, parts = 0;  // list positions per run; aligned mode: CTAs per item
-  {
-    int total = 0, items = 0, longest = 0;
-    bool odd_len = false;
-    for (int b = lane; b < p.seqs; b += 32) {
-      const Seq s = load_seq<C::kRows>(p, b);
-      odd_len |= __ldg(p.kv_len + b) != s.kv;
-      const int n = s.groups * p.kv_heads;
-      total += item_size(s) * n;
-      items += n;
-      longest = max(longest, s.pages);
-    }
-    if (odd_len && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, kKvErrLength);
-    total = __reduce_add_sync(0xffffffffu, total);
-    items = __reduce_add_sync(0xffffffffu, items);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (items == 0) return;  // (every return here is the whole CTA's)
-    const int cta = blockIdx.x, grid = gridDim.x;
-    per = div_pos(total + grid - 1, grid);
-    // Aligned: every item in `parts` equal parts, when that makes no run much
-    // longer than an equal share, each part at least two pages per team
-    // (shorter ones save less than the join costs).
-    if (items <= grid) {
-      const int k = max(min(div_pos(grid, items), longest / (2 * C::kTeams)), 1);
-      if (div_pos(longest + k - 1, k) <= max(per + per / 8, 2 * C::kTeams)) parts = k;
-    }
-    // list: no run shorter than one page per team while items have as many
-    if (parts == 0) per = max(per, min(C::kTeams, div_pos(total, items)));
-    const int at = parts ? div_pos(cta, parts) : min(per * cta, total);  // item, or list position
-    if (at >= (parts ? items : total)) return;
-    int base = 0, seen = 0;  // list position and units before the current 32 sequences
-    for (int b0 = 0;; b0 += 32) {
-      Seq s = {};
-      if (b0 + lane < p.seqs) s = load_seq<C::kRows>(p, b0 + lane);
-      const int n = s.groups * p.kv_heads, size = item_size(s) * n, step = parts ? n : size;
-      const int all = __reduce_add_sync(0xffffffffu, step);
-      if (at >= seen + all && b0 + 32 < p.seqs) {
-        seen += all;
-        base += __reduce_add_sync(0xffffffffu, size);
-        continue;
-      }
-      int upto = step, pos = size;  // inclusive sums over the lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, upto, o), v = __shfl_up_sync(0xffffffffu, pos, o);
-        if (lane >= o) {
-          upto += u;
-          pos += v;
-        }
-      }
-      const int who = __ffs(__ballot_sync(0xffffffffu, at < seen + upto)) - 1;  // (there is one)
-      walk.b = b0 + who;
-      walk.base = base + __shfl_sync(0xffffffffu, pos - size, who);
-      seen += __shfl_sync(0xffffffffu, upto - step, who);
-      walk.s.q0 = __shfl_sync(0xffffffffu, s.q0, who);
-      walk.s.n = __shfl_sync(0xffffffffu, s.n, who);
-      walk.s.kv = __shfl_sync(0xffffffffu, s.kv, who);
-      walk.s.sink_pages = __shfl_sync(0xffffffffu, s.sink_pages, who);
-      walk.s.lo = __shfl_sync(0xffffffffu, s.lo, who);
-      walk.s.pages = __shfl_sync(0xffffffffu, s.pages, who);
-      walk.s.groups = __shfl_sync(0xffffffffu, s.groups, who);
-      break;
-    }
-    if (parts) {
-      const int len = div_pos(walk.s.pages + parts - 1, parts);
-      const int first = (cta - at * parts) * len;
-      if (first >= walk.s.pages) return;
-      walk.w = walk.base + (at - seen) * item_size(walk.s) + kItemCost + first;
-      walk.end = walk.w + min(len, walk.s.pages - first);
-    } else {
-      walk.w = at;
-      walk.end = min(at + per, total);
-    }
-  }
+  int per, parts;
+  if (!find_run<C::kRows>(p, C::kTeams, lane, warp, walk, per, parts)) return;  // the whole CTA
 
   // ---- the query rows of a segment, raw: 4 dims of each 16 per thread
   uint2 raw[NT][kKC];
@@ -392,13 +546,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
     }
     const int id = __shfl_sync(0xffffffffu, ids, ahead_at);
     if (RW > 1 && filled >= C::kTeamSlots) {
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait(empty(fill_slot), fill_phase, abort_flag, kWaitLimitNs))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(empty(fill_slot), fill_phase, abort_flag))) {
         dead = true;
         if (p.status) atomicOr(p.status, kKvErrTimeout);
         return;
       }
     }
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t bar = full(fill_slot);
       meta[slot0 + fill_slot] = id;
       if (id < 0) {
@@ -428,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
   int use_slot = 0;
   uint32_t use_phase = 0;
   const auto wait_full = [&]() {
-    if (!__all_sync(0xffffffffu, ptx::mbar_wait(full(use_slot), use_phase, abort_flag, kWaitLimitNs))) {
+    if (!__all_sync(0xffffffffu, mbar_wait(full(use_slot), use_phase, abort_flag))) {
       dead = true;
       if (p.status) atomicOr(p.status, kKvErrTimeout);
       return -1;
@@ -443,18 +597,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
       use_phase ^= 1;
     }
     if (rw == 0) fill();
-  };
-
-  // four dims of a finished row
-  const auto store_row = [&](int q0, int head, int r, int d4, const float4& sum, float top, float den) {
-    const int token = by_group(p, r);
-    const size_t at = static_cast<size_t>(q0 + token) * (p.kv_heads * p.group) + head * p.group + r - token * p.group;
-    const float inv = den == 0.0f ? 0.0f : __frcp_rn(den);
-    __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(sum.x * inv, sum.y * inv),
-                                        __floats2bfloat162_rn(sum.z * inv, sum.w * inv)};
-    *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
-    if (d4 == 0 && p.lse)
-      p.lse[at] = den == 0.0f ? -INFINITY : (top + log2f(den) - kLog2P) * 0.69314718055994531f;
   };
 
   // matrix-load rows of this lane: 8 rows x {16-byte chunk} per quarter warp
@@ -515,25 +657,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
         for (int j = 0; j < 4; ++j) o[nt][d][j] = 0.0f;
     }
 
-    const auto sees = [&](int token, int at) {
-      return token <= at && (p.window == 0 || token > at - p.window || token < p.sinks);
-    };
-
     for (int j = first + team; j < last; j += C::kTeams) {
       const int index = j < s.sink_pages ? j : s.lo + (j - s.sink_pages);
       const int t0 = index * kPageTokens, t1 = t0 + kPageTokens - 1;
-      // 0: no row of the tile sees any of the page, 1: every row sees all of it, 2: mixed
       int kind[NT];
       bool any = false, cut = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        kind[nt] = 2;
-        if (t1 <= pos_lo[nt] && (p.window == 0 || t0 > pos_hi[nt] - p.window || t1 < p.sinks))
-          kind[nt] = 1;
-        else if (t0 > pos_hi[nt] ||
-                 (p.window > 0 && t1 <= pos_lo[nt] - p.window && t0 >= p.sinks))
-          kind[nt] = 0;
-        if (row0 + nt * 8 >= rows) kind[nt] = 0;
+        kind[nt] = row0 + nt * 8 >= rows ? 0 : page_kind(p, t0, t1, pos_lo[nt], pos_hi[nt]);
         any |= kind[nt] != 0;
         cut |= kind[nt] == 2;
       }
@@ -581,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (!sees(t0 + mt * 16 + g + (i >> 1) * 8, pos[nt][i & 1]))
+                if (!sees(p, t0 + mt * 16 + g + (i >> 1) * 8, pos[nt][i & 1]))
                   sc[nt][mt][i] = -INFINITY;
           }
 #pragma unroll
@@ -592,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float f = factor[nt][c] * kscale;
+            const float f = fmaxf(factor[nt][c] * kscale, FLT_MIN);  // (never 0: masked scores are -inf)
             const float top = kind[nt] == 0 ? m[nt][c] : fmaxf(m[nt][c], mx * f);
             const float use = top == -INFINITY ? 0.0f : top;
             alpha[nt][c] = ex2(m[nt][c] - use);
@@ -663,8 +794,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int t = t0 + c * 16 + 2 * q;
-                keep[c] = (sees(t, at) ? 0x000000FFu : 0u) | (sees(t + 1, at) ? 0x0000FF00u : 0u) |
-                          (sees(t + 8, at) ? 0x00FF0000u : 0u) | (sees(t + 9, at) ? 0xFF000000u : 0u);
+                keep[c] = (sees(p, t, at) ? 0x000000FFu : 0u) | (sees(p, t + 1, at) ? 0x0000FF00u : 0u) |
+                          (sees(p, t + 8, at) ? 0x00FF0000u : 0u) | (sees(p, t + 9, at) ? 0xFF000000u : 0u);
               }
               const bool mine[2] = {pos[nt][0] == at, pos[nt][1] == at};
 #pragma unroll
@@ -700,16 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
 
     // ---- the segment's rows: join the teams, then write them out or to the workspace
     int c0 = 0, c1 = 0;
-    if (!whole) {
-      if (parts) {
-        c0 = div_pos(blockIdx.x, parts) * parts;
-        const int len = div_pos(s.pages + parts - 1, parts);
-        c1 = c0 + div_pos(s.pages + len - 1, len) - 1;
-      } else {
-        c0 = div_pos(item_start + kItemCost, per);
-        c1 = div_pos(item_start + kItemCost + s.pages - 1, per);
-      }
-    }
+    if (!whole) item_ctas(item_start, s.pages, per, parts, c0, c1);
     const int part_slot = static_cast<int>(blockIdx.x) == c0;
     float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + part_slot) * C::kRows * (D + 2);
     if (!whole && tid == 0) {
@@ -773,7 +895,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
           den += top == -INFINITY ? 0.0f : t_ml.y * ex2(t_ml.x - top);
         }
         if (whole) {
-          store_row(s.q0, head, r, d4, sum, top, den);
+          store_row<D>(p, s.q0, head, r, d4, sum, top, den, kLog2P);
         } else {
           const int lr = (w * NT + nt) * 8 + row;
           *reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + d4 * 4) = sum;
@@ -785,70 +907,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
     }
   }
 
-  // ---- items of several CTAs (a run has at most two): the last CTA to arrive
-  // joins their partial rows
-  if (shared[0].c1 >= 0 || shared[1].c1 >= 0) {  // uniform: written before the loop's last barrier
-    if (tid == 0) {
-      __threadfence();
-      for (int i = 0; i < 2; ++i) {
-        Shared& x = shared[i];
-        x.last = 0;
-        if (x.c1 < 0) continue;
-        if (atomicAdd(p.tickets + x.c0, 1) == x.c1 - x.c0) {
-          p.tickets[x.c0] = 0;
-          x.last = 1;
-        }
-      }
-      __threadfence();
-    }
-    __syncthreads();
-    for (int i = 0; i < 2; ++i) {
-      const Shared x = shared[i];
-      if (x.c1 < 0 || !x.last) continue;
-      const auto partial = [&](int c) {
-        return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * C::kRows * (D + 2);
-      };
-      // 4 dims of a row per thread; eight parts' loads in flight
-      const int count = min(C::kRows, x.rows - x.row0) * (D / 4);
-      for (int u = tid; u < count; u += C::kThreads) {
-        const int lr = u / (D / 4), d4 = u % (D / 4);
-        float top = -INFINITY, den = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int cb = x.c0; cb <= x.c1; cb += 8) {
-          float4 y[8];
-          float2 t[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* src = partial(min(cb + k, x.c1));
-            y[k] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(lr) * D) + d4);
-            t[k] = __ldcg(reinterpret_cast<const float2*>(src + C::kRows * D) + lr);
-          }
-          float high = top;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) high = fmaxf(high, t[k].x);
-          const float use = high == -INFINITY ? 0.0f : high;
-          const float keep = ex2(top - use);
-          top = high;
-          den *= keep;
-          sum.x *= keep;
-          sum.y *= keep;
-          sum.z *= keep;
-          sum.w *= keep;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (cb + k > x.c1) break;
-            const float w = ex2(t[k].x - use);
-            den = fmaf(t[k].y, w, den);
-            sum.x = fmaf(y[k].x, w, sum.x);
-            sum.y = fmaf(y[k].y, w, sum.y);
-            sum.z = fmaf(y[k].z, w, sum.z);
-            sum.w = fmaf(y[k].w, w, sum.w);
-          }
-        }
-        store_row(x.q0, x.head, x.row0 + lr, d4, sum, top, den);
-      }
-    }
-  }
+  join_shared<D, C::kRows>(p, shared, tid, C::kThreads, kLog2P);
 
   // Every copy issued has been waited for, as each page of the run is
   // consumed. After a wait that gave up, the copies in flight get their time

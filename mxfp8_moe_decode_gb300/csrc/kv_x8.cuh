@@ -103,6 +103,7 @@ struct AttnX8Params {
   float* lse;              // [tokens][q_heads] or null
   float* part;             // workspace: partial rows of items that several CTAs share
   int* tickets;            // workspace: [grid] CTAs of a shared item that are done (0 between calls)
+  void* records;           // workspace: [grid] the shared item that starts in a CTA (attn_wide.cuh)
   int* status;             // or null
   int tokens, seqs, max_pages, pages, kv_heads, group;
   unsigned group_magic;    // floor(2^32 / group) + 1 (unused for a group of 1)
