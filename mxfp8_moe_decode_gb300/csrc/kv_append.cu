@@ -46,27 +46,42 @@ __device__ __forceinline__ uint4 requant16(const uint4& v, float mul) {
                     requant4(v.w, mul));
 }
 
-// Largest finite magnitude among 8 bf16 values, as bf16 bits.
+// Largest magnitudes among 8 bf16 values, as two bf16 bit patterns; kFinite:
+// infinities and NaN left out.
+template <bool kFinite>
 __device__ __forceinline__ uint32_t amax_bits(const uint4& v, uint32_t a) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-    a = max(a, lo < 0x7F80u ? lo : 0u);
-    a = max(a, hi < 0x7F80u ? hi : 0u);
+    uint32_t m = w[j] & 0x7FFF7FFFu;
+    if (kFinite) m &= __vcmpltu2(m, 0x7F807F80u);
+    a = __vmaxu2(a, m);
   }
   return a;
 }
 
-__device__ __forceinline__ uint2 quant8(const uint4& v, float mul) {
+// 8 values times a power of two -> E4M3: exact in bf16 but for underflow, which
+// lies far below E4M3's smallest value; saturating, so that +-inf becomes
+// +-448, and NaN stays.
+__device__ __forceinline__ uint2 quant8(const uint4& v, __nv_bfloat162 mul) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
   uint32_t b[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = __bfloat1622float2(h[j]);
-    b[j] = e4m3x2(f.x * mul, f.y * mul);  // saturating: +-inf becomes +-448, NaN stays
+    const float2 f = __bfloat1622float2(__hmul2(h[j], mul));
+    b[j] = e4m3x2(f.x, f.y);
   }
   return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+}
+
+// The CTA's largest bf16 bit pattern.
+__device__ __forceinline__ uint32_t cta_max(uint32_t a, uint32_t* red) {
+  a = __reduce_max_sync(0xffffffffu, max(a >> 16, a & 0xFFFFu));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) a = max(a, red[i]);
+  return a;
 }
 
 template <int D>
@@ -75,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   constexpr int kMax = kPageTokens * kRowChunks / kThreads;        // chunks a thread holds
   constexpr int kPitch = D + 4;                                    // staged token row, bytes
   __shared__ __align__(16) uint8_t stage[kPageTokens * kPitch];
-  __shared__ uint32_t red[kThreads / 32];
+  __shared__ uint32_t red[2][kThreads / 32];
   const int tid = threadIdx.x;
   const int head = blockIdx.y, kv = blockIdx.z;
   ptx::griddep_wait();
@@ -93,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     int below = 0;
     for (int i0 = 0; i0 < p.seqs; i0 += kThreads) {
       const int i = i0 + tid;
+      if (i < p.seqs) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.start + i));  // read next
       const bool le = i < p.seqs &&
                       static_cast<long long>(min(max(p.cu_q[i], 0), p.tokens) / kPageTokens) +
                               2ll * i <= slot;
@@ -113,36 +129,40 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   const int base = page_index * kPageTokens;
   const int t0 = max(start, base), t1 = min(start + n, base + kPageTokens);
   if (t1 <= t0) return;
-  int page = -1;
-  if (page_index < p.max_pages)
-    page = p.page_table[static_cast<size_t>(b) * p.max_pages + page_index];
-  if (page < 0 || page >= p.pages) {
-    if (tid == 0 && p.status) atomicOr(p.status, page_index < p.max_pages ? kKvErrPage : kKvErrLength);
-    return;
-  }
   const int off = t0 - base;  // the page's earlier tokens
   const int count = t1 - t0;
   const long long ld = kv ? p.ldv : p.ldk;
   const __nv_bfloat16* src = (kv ? p.v : p.k) + (c0 + (t0 - start)) * ld + static_cast<long long>(head) * D;
-  const size_t owner = (static_cast<size_t>(page) * p.kv_heads + head) * 2 + kv;
-  uint8_t* img = p.blocks + owner * (static_cast<size_t>(kPageTokens) * D);
 
+  // the values are on their way while the page is looked up
   uint4 v[kMax];
-  uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < kMax; ++i) {
     const int c = tid + i * kThreads;
     v[i] = make_uint4(0, 0, 0, 0);
     if (c < count * kRowChunks)
       v[i] = __ldcs(reinterpret_cast<const uint4*>(src + (c / kRowChunks) * ld) + c % kRowChunks);
-    a = amax_bits(v[i], a);
   }
-  a = __reduce_max_sync(0xffffffffu, a);
-  if ((tid & 31) == 0) red[tid >> 5] = a;
-  const int had = off > 0 ? min(static_cast<int>(p.codes[owner]), 254) : 0;
-  __syncthreads();
+  int page = -1;
+  if (page_index < p.max_pages)
+    page = __ldg(p.page_table + static_cast<size_t>(b) * p.max_pages + page_index);
+  if (page < 0 || page >= p.pages) {
+    if (tid == 0 && p.status) atomicOr(p.status, page_index < p.max_pages ? kKvErrPage : kKvErrLength);
+    return;
+  }
+  const size_t owner = (static_cast<size_t>(page) * p.kv_heads + head) * 2 + kv;
+  uint8_t* img = p.blocks + owner * (static_cast<size_t>(kPageTokens) * D);
+  uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) a = max(a, red[i]);
+  for (int i = 0; i < kMax; ++i) a = amax_bits<false>(v[i], a);
+  const int had = off > 0 ? min(static_cast<int>(p.codes[owner]), 254) : 0;
+  a = cta_max(a, red[0]);
+  if (a >= 0x7F80u) {  // (uniform) a value that is not finite: once more without those
+    a = 0;
+#pragma unroll
+    for (int i = 0; i < kMax; ++i) a = amax_bits<true>(v[i], a);
+    a = cta_max(a, red[1]);
+  }
   const int code = max(had, mx_code(__uint_as_float(a << 16)));
   if (off > 0 && code > had) {
     // every byte is below 2^-10 from a shift of 19 on and rounds to zero, so
@@ -160,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     }
   }
   if (tid == 0) p.codes[owner] = static_cast<uint8_t>(code);
-  const float mul = mx_mul(code);
+  const __nv_bfloat162 mul = __float2bfloat162_rn(mx_mul(code));
   if (kv == 0) {
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {
