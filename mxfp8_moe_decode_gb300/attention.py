@@ -10,12 +10,14 @@ an int32 ``status`` tensor if one is passed (``KV_STATUS_*`` of :mod:`._lib`).
 
 from __future__ import annotations
 
+import ctypes
 import math
+import struct
 
 import torch
 
 from . import _lib
-from ._lib import ATTN_X8_WORKSPACE_BYTES, KV_PAGE_TOKENS, KvCache, KvSeqs, check
+from ._lib import ATTN_X8_WORKSPACE_BYTES, KV_PAGE_TOKENS, check
 
 
 def _rows(name: str, t: torch.Tensor, shape: tuple, device) -> int:
@@ -46,6 +48,25 @@ def _dense(name: str, t, shape: tuple, dtype, device) -> None:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+# moe_kv_cache and moe_kv_seqs as bytes in C layout
+_CACHE = struct.Struct("@PPiii")
+_SEQS = struct.Struct("@PPPiiii")
+_entry_points = None
+
+
+def _entries():
+    """The cache's two entry points with their structs passed as bytes."""
+    global _entry_points
+    if _entry_points is None:
+        L = _lib.lib()
+        append, attn = L["moe_kv_append_x8"], L["moe_attn_x8"]
+        for fn, ref in ((append, L.moe_kv_append_x8), (attn, L.moe_attn_x8)):
+            fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p, *ref.argtypes[2:]]
+            fn.restype = ref.restype
+        _entry_points = append, attn
+    return _entry_points
 
 
 def _call(name: str, fn, index: int, *args) -> None:
@@ -127,31 +148,36 @@ def kv_dequant_x8(blocks: torch.Tensor, codes: torch.Tensor) -> torch.Tensor:
 
 
 def _cache(blocks: torch.Tensor, codes: torch.Tensor):
-    if blocks.dim() != 4 or not blocks.is_cuda or blocks.dtype != torch.uint8 or not blocks.is_contiguous() \
-            or blocks.shape[2] != 2 or blocks.shape[3] % KV_PAGE_TOKENS:
+    """(packed moe_kv_cache, kv_heads, head_dim, device)"""
+    shape, dev = blocks.shape, blocks.device
+    if len(shape) != 4 or not blocks.is_cuda or blocks.dtype != torch.uint8 or not blocks.is_contiguous() \
+            or shape[2] != 2 or shape[3] % KV_PAGE_TOKENS:
         raise ValueError("blocks must be a contiguous CUDA uint8 [pages, kv_heads, 2, 64 * head_dim] tensor")
-    pages, heads, _, size = blocks.shape
-    _dense("codes", codes, (pages, heads, 2), torch.uint8, blocks.device)
-    return KvCache(blocks.data_ptr(), codes.data_ptr(), pages, heads, size // KV_PAGE_TOKENS)
+    pages, heads, _, size = shape
+    _dense("codes", codes, (pages, heads, 2), torch.uint8, dev)
+    d = size // KV_PAGE_TOKENS
+    return _CACHE.pack(blocks.data_ptr(), codes.data_ptr(), pages, heads, d), heads, d, dev
 
 
-def _seqs(page_table, lens, cu_q, tokens: int, max_q: int, device):
-    if page_table.dim() != 2:
+def _seqs(page_table, lens, cu_q, tokens: int, max_q: int, device) -> bytes:
+    """Packed moe_kv_seqs."""
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be an int32 [seqs, max_pages] tensor")
-    n, width = page_table.shape
-    _dense("page_table", page_table, (n, width), torch.int32, device)
+    n = shape[0]
+    _dense("page_table", page_table, shape, torch.int32, device)
     _dense("lens", lens, (n,), torch.int32, device)
     if cu_q is None:
         if tokens != n:
             raise ValueError(f"{tokens} rows for {n} sequences: without cu_q each has one")
-        return KvSeqs(page_table.data_ptr(), lens.data_ptr(), None, n, tokens, width, max_q)
-    _dense("cu_q", cu_q, (n + 1,), torch.int32, device)
-    return KvSeqs(page_table.data_ptr(), lens.data_ptr(), cu_q.data_ptr(), n, tokens, width, max_q)
+        starts = 0
+    else:
+        _dense("cu_q", cu_q, (n + 1,), torch.int32, device)
+        starts = cu_q.data_ptr()
+    return _SEQS.pack(page_table.data_ptr(), lens.data_ptr(), starts, n, tokens, shape[1], max_q)
 
 
 def _status(status, device):
-    if status is None:
-        return None
     _dense("status", status, (1,), torch.int32, device)
     return status.data_ptr()
 
@@ -166,15 +192,15 @@ def kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, k: torch.Tensor, v: 
     (tokens each sequence has already), cu_q int32 [seqs + 1] (rows of each
     sequence; None: one each). Changes blocks and codes in place and returns them.
     """
-    cache = _cache(blocks, codes)
-    dev = blocks.device
+    cache, heads, d, dev = _cache(blocks, codes)
     if k.dim() != 3:
         raise ValueError("k must be a bf16 [tokens, kv_heads, head_dim] tensor")
-    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    tokens = k.shape[0]
+    shape = (tokens, heads, d)
     ldk, ldv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
-    seqs = _seqs(page_table, start, cu_q, k.shape[0], 1, dev)
-    st = _status(status, dev)
-    _call("moe_kv_append_x8", _lib.lib().moe_kv_append_x8, dev.index, cache, seqs, k.data_ptr(), ldk,
+    seqs = _seqs(page_table, start, cu_q, tokens, 1, dev)
+    st = None if status is None else _status(status, dev)
+    _call("moe_kv_append_x8", _entries()[0], dev.index, cache, seqs, k.data_ptr(), ldk,
           v.data_ptr(), ldv, st)
     return blocks, codes
 
@@ -204,18 +230,17 @@ def attn_x8(q: torch.Tensor, blocks: torch.Tensor, codes: torch.Tensor, page_tab
     calls this often keeps a ``workspace`` (:func:`attn_x8_workspace`), one for
     each stream; without one, a zeroed one is allocated for the call.
     """
-    cache = _cache(blocks, codes)
-    dev = blocks.device
+    cache, _, d, dev = _cache(blocks, codes)
     if q.dim() != 3:
         raise ValueError("q must be a bf16 [tokens, q_heads, head_dim] tensor")
-    tokens, heads, d = q.shape
-    ldq = _rows("q", q, (tokens, heads, cache.head_dim), dev)
+    tokens, heads, _ = q.shape
+    ldq = _rows("q", q, (tokens, heads, d), dev)
     if cu_q is None:
         max_q = 1
     elif max_q is None:
         max_q = max(tokens, 1)
     seqs = _seqs(page_table, kv_len, cu_q, tokens, max_q, dev)
-    st = _status(status, dev)
+    st = None if status is None else _status(status, dev)
     if out is None:
         out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
     else:
@@ -226,7 +251,7 @@ def attn_x8(q: torch.Tensor, blocks: torch.Tensor, codes: torch.Tensor, page_tab
         workspace = attn_x8_workspace(dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _call("moe_attn_x8", _lib.lib().moe_attn_x8, dev.index, cache, seqs, q.data_ptr(), ldq, heads,
+    _call("moe_attn_x8", _entries()[1], dev.index, cache, seqs, q.data_ptr(), ldq, heads,
           1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(),
           None if lse is None else lse.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), st)
