@@ -846,6 +846,49 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
   if (tid == 0) static_cast<Shared*>(p.records)[blockIdx.x] = misc->shared[1];
 }
 
+// Four dims of a row of a shared item, from its parts in CTA order. A part holds
+// four dims of all rows after another, then each row's {reference, sum}.
+template <int D, int kRows, int kBatch>
+__device__ __forceinline__ void join_row(const AttnX8Params& p, const Shared& x, int lr, int d4, float log2_scale) {
+  const auto partial = [&](int c) {
+    return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
+  };
+  float top = -INFINITY, den = 0.0f;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int cb = x.c0; cb <= x.c1; cb += kBatch) {  // kBatch parts' loads in flight
+    float4 y[kBatch];
+    float2 t[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* src = partial(min(cb + k, x.c1));
+      y[k] = __ldcg(reinterpret_cast<const float4*>(src) + (d4 * kRows + lr));
+      t[k] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + lr);
+    }
+    float high = top;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) high = fmaxf(high, t[k].x);
+    const float use = high == -INFINITY ? 0.0f : high;
+    const float keep = ex2(top - use);
+    top = high;
+    den *= keep;
+    sum.x *= keep;
+    sum.y *= keep;
+    sum.z *= keep;
+    sum.w *= keep;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (cb + k > x.c1) break;
+      const float w = ex2(t[k].x - use);
+      den = fmaf(t[k].y, w, den);
+      sum.x = fmaf(y[k].x, w, sum.x);
+      sum.y = fmaf(y[k].y, w, sum.y);
+      sum.z = fmaf(y[k].z, w, sum.z);
+      sum.w = fmaf(y[k].w, w, sum.w);
+    }
+  }
+  store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, log2_scale);
+}
+
 // The rows of items that several CTAs share, joined with the whole GPU behind
 // the kernel above (in it, the few CTAs that arrive last would take longer for
 // up to 256 rows than all the rest: 110 of 207 us for 240 rows in 19 parts).
@@ -860,7 +903,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) attn_wide_join_kernel(const
   const Shared x = static_cast<const Shared*>(p.records)[blockIdx.x];
   const int lr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
   if (x.c1 < 0 || x.row0 + lr >= x.rows) return;
-  join_row<D, WideCfg<D>::kRows, true>(p, x, lr, threadIdx.x / kJoinRows, kLog2PWide);
+  join_row<D, WideCfg<D>::kRows, 8>(p, x, lr, threadIdx.x / kJoinRows, kLog2PWide);
 }
 
 template <int D>

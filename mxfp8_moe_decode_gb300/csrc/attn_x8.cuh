@@ -289,11 +289,13 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
     Seq s = {};
     if (b0 + lane < p.seqs) s = load_seq<kRows>(p, b0 + lane);
     const int n = s.groups * p.kv_heads, size = item_size(s) * n, step = parts ? n : size;
-    const int all = __reduce_add_sync(0xffffffffu, step);
-    if (at >= seen + all && b0 + 32 < p.seqs) {
-      seen += all;
-      base += __reduce_add_sync(0xffffffffu, size);
-      continue;
+    if (b0 + 32 < p.seqs) {
+      const int all = __reduce_add_sync(0xffffffffu, step);
+      if (at >= seen + all) {
+        seen += all;
+        base += __reduce_add_sync(0xffffffffu, size);
+        continue;
+      }
     }
     int upto = step, pos = size;  // inclusive sums over the lanes
 #pragma unroll
@@ -378,76 +380,100 @@ __device__ __forceinline__ void store_row(const AttnX8Params& p, int q0, int hea
     p.lse[at] = den == 0.0f ? -INFINITY : (top + log2f(den) - log2_scale) * 0.69314718055994531f;
 }
 
-// Four dims of a row of a shared item, from its parts in CTA order. A part holds
-// its rows' sums, row by row or (kCols) four dims of all rows after another,
-// and then each row's {m, l}.
-template <int D, int kRows, bool kCols = false>
-__device__ __forceinline__ void join_row(const AttnX8Params& p, const Shared& x, int lr, int d4, float log2_scale) {
-  const auto partial = [&](int c) {
-    return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
-  };
-  float top = -INFINITY, den = 0.0f;
-  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int cb = x.c0; cb <= x.c1; cb += 8) {  // eight parts' loads in flight
-    float4 y[8];
-    float2 t[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float* src = partial(min(cb + k, x.c1));
-      y[k] = __ldcg(reinterpret_cast<const float4*>(src) + (kCols ? d4 * kRows + lr : lr * (D / 4) + d4));
-      t[k] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + lr);
-    }
-    float high = top;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) high = fmaxf(high, t[k].x);
-    const float use = high == -INFINITY ? 0.0f : high;
-    const float keep = ex2(top - use);
-    top = high;
-    den *= keep;
-    sum.x *= keep;
-    sum.y *= keep;
-    sum.z *= keep;
-    sum.w *= keep;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (cb + k > x.c1) break;
-      const float w = ex2(t[k].x - use);
-      den = fmaf(t[k].y, w, den);
-      sum.x = fmaf(y[k].x, w, sum.x);
-      sum.y = fmaf(y[k].y, w, sum.y);
-      sum.z = fmaf(y[k].z, w, sum.z);
-      sum.w = fmaf(y[k].w, w, sum.w);
-    }
-  }
-  store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, log2_scale);
-}
-
 // The CTA's end: items of several CTAs (a run has at most two). The last CTA
-// to arrive joins their partial rows. All threads call this after a barrier
-// behind their partial rows.
-template <int D, int kRows>
-__device__ __forceinline__ void join_shared(const AttnX8Params& p, Shared* shared, int tid, int threads,
+// to arrive joins their partial rows, in the order of the CTAs: each warp the
+// parts c0 + w, c0 + w + kWarps, ... of 256 x 4 dims at a time, then the warps'
+// sums through shared memory (`space`, 256 x kWarps x 24 bytes that nothing
+// uses any more). All threads call this after a barrier behind their partial
+// rows.
+template <int D, int kRows, int kWarps>
+__device__ __forceinline__ void join_shared(const AttnX8Params& p, Shared* shared, uint8_t* space, int tid,
                                             float log2_scale) {
   if (shared[0].c1 < 0 && shared[1].c1 < 0) return;  // (the same in every thread)
-  if (tid == 0) {
-    __threadfence();
-    for (int i = 0; i < 2; ++i) {
-      Shared& x = shared[i];
-      x.last = 0;
-      if (x.c1 < 0) continue;
-      if (atomicAdd(p.tickets + x.c0, 1) == x.c1 - x.c0) {
+  if (tid < 2) {
+    Shared& x = shared[tid];
+    x.last = 0;
+    if (x.c1 >= 0) {
+      // releases the CTA's partial rows (the barrier before orders them) and
+      // acquires those of the CTAs that came earlier
+      int done;
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(done) : "l"(p.tickets + x.c0) : "memory");
+      if (done == x.c1 - x.c0) {
         p.tickets[x.c0] = 0;
         x.last = 1;
       }
     }
-    __threadfence();
   }
   __syncthreads();
+  constexpr int kUnits = 256, kPer = kUnits / 32;  // units of 4 dims, per lane
+  float4* sums = reinterpret_cast<float4*>(space);                      // [warp][kUnits]
+  float2* mls = reinterpret_cast<float2*>(sums + kWarps * kUnits);
+  const int warp = tid >> 5, lane = tid & 31;
   for (int i = 0; i < 2; ++i) {
     const Shared x = shared[i];
     if (x.c1 < 0 || !x.last) continue;
     const int count = min(kRows, x.rows - x.row0) * (D / 4);
-    for (int u = tid; u < count; u += threads) join_row<D, kRows>(p, x, u / (D / 4), u % (D / 4), log2_scale);
+    for (int u0 = 0; u0 < count; u0 += kUnits) {
+      float4 sum[kPer];
+      float top[kPer], den[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        sum[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        top[k] = -INFINITY;
+        den[k] = 0.0f;
+      }
+#pragma unroll 2
+      for (int c = x.c0 + warp; c <= x.c1; c += kWarps) {
+        const float* part = p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
+        float4 y[kPer];
+        float2 t[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int u = min(u0 + lane + 32 * k, count - 1);
+          y[k] = __ldcg(reinterpret_cast<const float4*>(part) + u);
+          t[k] = __ldcg(reinterpret_cast<const float2*>(part + kRows * D) + u / (D / 4));
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const float high = fmaxf(top[k], t[k].x), use = high == -INFINITY ? 0.0f : high;
+          const float keep = ex2(top[k] - use), w = ex2(t[k].x - use);
+          top[k] = high;
+          den[k] = den[k] * keep + t[k].y * w;
+          sum[k].x = sum[k].x * keep + y[k].x * w;
+          sum[k].y = sum[k].y * keep + y[k].y * w;
+          sum[k].z = sum[k].z * keep + y[k].z * w;
+          sum[k].w = sum[k].w * keep + y[k].w * w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        sums[warp * kUnits + lane + 32 * k] = sum[k];
+        mls[warp * kUnits + lane + 32 * k] = make_float2(top[k], den[k]);
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int u = tid; u < kUnits && u0 + u < count; u += 32 * kWarps) {
+        float high = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) high = fmaxf(high, mls[w * kUnits + u].x);
+        const float use = high == -INFINITY ? 0.0f : high;
+        float all = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = sums[w * kUnits + u];
+          const float2 t = mls[w * kUnits + u];
+          const float k = ex2(t.x - use);
+          all = fmaf(t.y, k, all);
+          o.x = fmaf(y.x, k, o.x);
+          o.y = fmaf(y.y, k, o.y);
+          o.z = fmaf(y.z, k, o.z);
+          o.w = fmaf(y.w, k, o.w);
+        }
+        store_row<D>(p, x.q0, x.head, x.row0 + (u0 + u) / (D / 4), (u0 + u) % (D / 4), o, high, all, log2_scale);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -907,7 +933,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
     }
   }
 
-  join_shared<D, C::kRows>(p, shared, tid, C::kThreads, kLog2P);
+  join_shared<D, C::kRows, C::kWarps>(p, shared, smem, tid, kLog2P);
 
   // Every copy issued has been waited for, as each page of the run is
   // consumed. After a wait that gave up, the copies in flight get their time
