@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
   if (warp == 0) {
     Walk w;
     int per, parts;
-    const bool work = find_run<C::kRows>(p, 2, lane, warp, w, per, parts);
+    const bool work = find_run<C::kRows, 1>(p, 2, lane, warp, w, per, parts);
     if (lane == 0) {
       misc->walk = w;
       misc->per = per;

@@ -63,7 +63,7 @@ namespace attn {
 
 constexpr uint32_t kRingBytes = 196608;
 constexpr float kLog2P = 14.0f;  // P is held times 2^14
-constexpr int kItemCost = 8;     // starting and joining an item costs about as much as its pages
+constexpr int kItemCost = 10;    // starting and joining an item costs about as much as its pages
 
 template <int D, int NT, int RW>
 struct Cfg {
@@ -251,8 +251,10 @@ __device__ __forceinline__ bool next_segment(const AttnX8Params& p, Walk& k) {
 // at a time (nothing to wait for but the lengths): once over them for the
 // list's length, once more to the run's start. False: nothing to do (the same
 // in every warp). `teams`: pages that a CTA works on at once. parts: CTAs per
-// item (aligned runs), or 0 and then per: list positions per run.
-template <int kRows>
+// item (aligned runs), or 0 and then per: list positions per run. kUneven: how
+// much longer than others a run may be, in eighths (bandwidth goes where pages
+// are left, the time of products does not).
+template <int kRows, int kUneven>
 __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int lane, int warp, Walk& walk,
                                          int& per, int& parts) {
   parts = 0;
@@ -273,12 +275,13 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
   if (items == 0) return false;
   const int cta = blockIdx.x, grid = gridDim.x;
   per = div_pos(total + grid - 1, grid);
-  // Aligned: every item in `parts` equal parts, when that makes no run much
-  // longer than an equal share, each part at least two pages per team
-  // (shorter ones save less than the join costs).
+  // Aligned: every item in `parts` equal parts, when that makes no run longer
+  // than an equal share of the pages by more than kUneven eighths, each part
+  // at least two pages per team (shorter ones save less than the join costs).
   if (items <= grid) {
+    const int share = div_pos(total - items * kItemCost, grid);
     const int k = max(min(div_pos(grid, items), longest / (2 * teams)), 1);
-    if (div_pos(longest + k - 1, k) <= max(per + per / 8, 2 * teams)) parts = k;
+    if (div_pos(longest + k - 1, k) <= max(share + share * kUneven / 8, 2 * teams)) parts = k;
   }
   // list: no run shorter than one page per team while items have as many
   if (parts == 0) per = max(per, min(teams, div_pos(total, items)));
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
   // ---- this CTA's run
   Walk walk;
   int per, parts;
-  if (!find_run<C::kRows>(p, C::kTeams, lane, warp, walk, per, parts)) return;  // the whole CTA
+  if (!find_run<C::kRows, 3>(p, C::kTeams, lane, warp, walk, per, parts)) return;  // the whole CTA
 
   // ---- the query rows of a segment, raw: 4 dims of each 16 per thread
   uint2 raw[NT][kKC];
