@@ -607,29 +607,35 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
       const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
       const bool idle = r - lane >= rows;  // no row of this warp
 
-      // the codes of the next 32 pages, one per lane
-      const auto page_codes = [&](int j) {
+      // the ids and then the codes of the next 32 pages, one per lane
+      const auto page_id = [&](int j) {
         if (j >= walk.last || s.kv == 0) return -1;
         const int index = j < s.sink_pages ? j : s.lo + (j - s.sink_pages);
-        const int id = __ldg(p.page_table + static_cast<size_t>(walk.b) * p.max_pages + index);
+        return __ldg(p.page_table + static_cast<size_t>(walk.b) * p.max_pages + index);
+      };
+      const auto page_codes = [&](int id) {
         if (id < 0 || id >= p.pages) return -1;
         return static_cast<int>(__ldg(reinterpret_cast<const unsigned short*>(p.codes) +
                                       static_cast<size_t>(id) * p.kv_heads + walk.head));
       };
-
-      if (!make_rows(walk, warp - 4, seg) || !wait(bars->q_full, seg)) {
+      const int id32 = page_id(walk.first + lane);
+      if (!make_rows(walk, warp - 4, seg)) {
+        ok = false;
+        break;
+      }
+      int codes32 = page_codes(id32);
+      if (!wait(bars->q_full, seg)) {
         ok = false;
         break;
       }
       const float factor = r < rows ? reinterpret_cast<const float*>(smem + C::kOffFactor)[lr] : 0.0f;
 
-      int codes32 = page_codes(walk.first + lane);
       float ref = -INFINITY, l = 0.0f;
       int vref = 0;       // the value code that P is relative to
       bool begun = false; // some page of this warp's rows was not all masked
       int own = 0;        // pages of this segment taken
       for (int i = 0; i < pages; ++i) {
-        if (i > 0 && (i & 31) == 0) codes32 = page_codes(walk.first + i + lane);
+        if (i > 0 && (i & 31) == 0) codes32 = page_codes(page_id(walk.first + i + lane));
         if (split && (i & 1) != t) continue;
         const int codes = __shfl_sync(0xffffffffu, codes32, i & 31);
         const int j = walk.first + i;
@@ -903,7 +909,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) attn_wide_join_kernel(const
   const Shared x = static_cast<const Shared*>(p.records)[blockIdx.x];
   const int lr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
   if (x.c1 < 0 || x.row0 + lr >= x.rows) return;
-  join_row<D, WideCfg<D>::kRows, 8>(p, x, lr, threadIdx.x / kJoinRows, kLog2PWide);
+  join_row<D, WideCfg<D>::kRows, 4>(p, x, lr, threadIdx.x / kJoinRows, kLog2PWide);
 }
 
 template <int D>
