@@ -61,13 +61,16 @@
 namespace moe {
 namespace attn {
 
-constexpr uint32_t kRingBytes = 196608;
 constexpr float kLog2P = 14.0f;  // P is held times 2^14
 constexpr int kItemCost = 10;    // starting and joining an item costs about as much as its pages
 
 template <int D, int NT, int RW>
 struct Cfg {
-  static constexpr int kWarps = D == 256 ? 3 : 6;
+  // Two slots a team at least: 12 pages of 16 KB (D = 128) for six teams; of the
+  // 32 KB pages of D = 256 six for three teams of one warp or two teams of two,
+  // four for two teams of three.
+  static constexpr int kWarps = D == 256 && RW == 1 ? 3 : D == 256 && RW == 2 ? 4 : 6;
+  static constexpr uint32_t kRingBytes = D == 256 && RW == 3 ? 131072 : 196608;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTeams = kWarps / RW;
   static constexpr int kRows = 8 * NT * RW;              // rows of a row group
