@@ -852,64 +852,107 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
   if (tid == 0) static_cast<Shared*>(p.records)[blockIdx.x] = misc->shared[1];
 }
 
-// Four dims of a row of a shared item, from its parts in CTA order. A part holds
-// four dims of all rows after another, then each row's {reference, sum}.
-template <int D, int kRows, int kBatch>
-__device__ __forceinline__ void join_row(const AttnX8Params& p, const Shared& x, int lr, int d4, float log2_scale) {
-  const auto partial = [&](int c) {
-    return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
-  };
-  float top = -INFINITY, den = 0.0f;
-  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int cb = x.c0; cb <= x.c1; cb += kBatch) {  // kBatch parts' loads in flight
-    float4 y[kBatch];
-    float2 t[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float* src = partial(min(cb + k, x.c1));
-      y[k] = __ldcg(reinterpret_cast<const float4*>(src) + (d4 * kRows + lr));
-      t[k] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + lr);
-    }
-    float high = top;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) high = fmaxf(high, t[k].x);
-    const float use = high == -INFINITY ? 0.0f : high;
-    const float keep = ex2(top - use);
-    top = high;
-    den *= keep;
-    sum.x *= keep;
-    sum.y *= keep;
-    sum.z *= keep;
-    sum.w *= keep;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (cb + k > x.c1) break;
-      const float w = ex2(t[k].x - use);
-      den = fmaf(t[k].y, w, den);
-      sum.x = fmaf(y[k].x, w, sum.x);
-      sum.y = fmaf(y[k].y, w, sum.y);
-      sum.z = fmaf(y[k].z, w, sum.z);
-      sum.w = fmaf(y[k].w, w, sum.w);
-    }
-  }
-  store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, log2_scale);
-}
-
 // The rows of items that several CTAs share, joined with the whole GPU behind
 // the kernel above (in it, the few CTAs that arrive last would take longer for
 // up to 256 rows than all the rest: 110 of 207 us for 240 rows in 19 parts).
-// Block (c, y): rows 16 y .. of the item that starts in CTA c and goes on,
-// neighbouring lanes on neighbouring rows. (A list of the items that fewer
-// blocks walk in turn was slower, 46.6 against 40.2 us for 48 items.)
-constexpr int kJoinRows = 16;
+// A part holds four dims of all rows after another, then each row's
+// {reference, sum}. A unit is kJoinRows rows of an item: four dims of a row per
+// thread, neighbouring lanes on neighbouring rows, the item's parts in turn to
+// kJoinGroups groups of threads whose sums are joined through shared memory (the
+// order of the sums depends on nothing but the parts' number). The blocks take
+// units in turn.
+constexpr int kJoinThreads = 512, kJoinGroups = 2, kJoinBatch = 5, kJoinBlocks = 2;
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * D / 4) attn_wide_join_kernel(const AttnX8Params p) {
+__global__ void __launch_bounds__(kJoinThreads) attn_wide_join_kernel(const AttnX8Params p) {
+  const int ctas = gridDim.x / kJoinBlocks;  // of the kernel above
+  constexpr int kRows = WideCfg<D>::kRows, kMembers = kJoinThreads / kJoinGroups;
+  constexpr int kJoinRows = kMembers / (D / 4);
+  __shared__ int warp_units[kJoinThreads / 32];
+  __shared__ int4 found;  // {record, first row, -, -}
+  __shared__ float4 sums[kJoinGroups - 1][kMembers];
+  __shared__ float2 tops[kJoinGroups - 1][kMembers];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = tid / kMembers, member = tid % kMembers;
+  const int d4 = member / kJoinRows;
+  const Shared* records = static_cast<const Shared*>(p.records);
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const Shared x = static_cast<const Shared*>(p.records)[blockIdx.x];
-  const int lr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
-  if (x.c1 < 0 || x.row0 + lr >= x.rows) return;
-  join_row<D, WideCfg<D>::kRows, 4>(p, x, lr, threadIdx.x / kJoinRows, kLog2PWide);
+  // where the units of record `tid` begin
+  int mine = 0;
+  if (tid < ctas && __ldcg(&records[tid].c1) >= 0)
+    mine = (min(__ldcg(&records[tid].rows) - __ldcg(&records[tid].row0), kRows) + kJoinRows - 1) / kJoinRows;
+  int end = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += x;
+  }
+  if (lane == 31) warp_units[warp] = end;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < warp) end += warp_units[w];
+    total += warp_units[w];
+  }
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    if (u >= end - mine && u < end) found = make_int4(tid, (u - (end - mine)) * kJoinRows, 0, 0);
+    __syncthreads();
+    const Shared x = records[found.x];
+    const int lr = found.y + member % kJoinRows;
+    const bool real = x.row0 + lr < x.rows && lr < kRows;
+    float top = -INFINITY, den = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (real) {
+      const auto partial = [&](int c) {
+        return p.part + (static_cast<size_t>(c) * 2 + (c == x.c0)) * kRows * (D + 2);
+      };
+      for (int cb = x.c0 + group; cb <= x.c1; cb += kJoinBatch * kJoinGroups) {  // a batch's loads in flight
+        float4 y[kJoinBatch];
+        float2 t[kJoinBatch];
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+          if (cb + k * kJoinGroups > x.c1) break;
+          const float* src = partial(cb + k * kJoinGroups);
+          y[k] = __ldcg(reinterpret_cast<const float4*>(src) + (d4 * kRows + lr));
+          t[k] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + lr);
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+          if (cb + k * kJoinGroups > x.c1) break;
+          const float high = fmaxf(top, t[k].x), use = high == -INFINITY ? 0.0f : high;
+          const float keep = ex2(top - use), w = ex2(t[k].x - use);
+          top = high;
+          den = fmaf(t[k].y, w, den * keep);
+          sum.x = fmaf(y[k].x, w, sum.x * keep);
+          sum.y = fmaf(y[k].y, w, sum.y * keep);
+          sum.z = fmaf(y[k].z, w, sum.z * keep);
+          sum.w = fmaf(y[k].w, w, sum.w * keep);
+        }
+      }
+    }
+    if (group > 0) {
+      sums[group - 1][member] = sum;
+      tops[group - 1][member] = make_float2(top, den);
+    }
+    __syncthreads();
+    if (group == 0 && real) {
+#pragma unroll
+      for (int k = 0; k < kJoinGroups - 1; ++k) {
+        const float4 y = sums[k][member];
+        const float2 t = tops[k][member];
+        const float high = fmaxf(top, t.x), use = high == -INFINITY ? 0.0f : high;
+        const float keep = ex2(top - use), w = ex2(t.x - use);
+        top = high;
+        den = fmaf(t.y, w, den * keep);
+        sum.x = fmaf(y.x, w, sum.x * keep);
+        sum.y = fmaf(y.y, w, sum.y * keep);
+        sum.z = fmaf(y.z, w, sum.z * keep);
+        sum.w = fmaf(y.w, w, sum.w * keep);
+      }
+      store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, kLog2PWide);
+    }
+  }
 }
 
 template <int D>
@@ -925,7 +968,7 @@ cudaError_t launch_wide(const AttnX8Params& p, int device, int grid, cudaStream_
   }
   const cudaError_t e = launch_pdl(attn_wide_kernel<D>, dim3(grid), dim3(C::kThreads), C::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_wide_join_kernel<D>, dim3(grid, C::kRows / kJoinRows), dim3(kJoinRows * D / 4), 0, s, p);
+  return launch_pdl(attn_wide_join_kernel<D>, dim3(kJoinBlocks * grid), dim3(kJoinThreads), 0, s, p);
 }
 
 }  // namespace attn
