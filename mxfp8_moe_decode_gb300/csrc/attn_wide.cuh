@@ -383,9 +383,10 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
 
   if (work && warp < 2) {
     // ------------------------------------------------------------ MMA issuer of tile t
-    // One thread. It goes through every page: the scores of the next page of
-    // its own are issued before the value product of the present one; pages of
-    // the other tile alone it only releases.
+    // One thread. It goes through every page twice, for the scores (up to two
+    // pages of its own ahead) and for the value products, and issues whichever
+    // is ready, value products first; pages of the other tile alone it only
+    // releases.
     const int t = warp;
     if (elect_one()) {
       const auto wait1 = [&](uint64_t& b, uint32_t parity) {
@@ -393,6 +394,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         if (p.status) atomicOr(p.status, kKvErrTimeout);
         return false;
       };
+      const auto ready = [&](uint64_t& b, uint32_t parity) { return mbar_test(bar(b), parity & 1); };
       const uint32_t tile = tmem + t * 256;
       int slot = 0, vb = 0, seg = 0;
       uint32_t slot_phase = 0, v_phase = 0;
@@ -404,80 +406,95 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         const uint32_t qb = sbase + C::kOffQ + (split ? 0 : 2 * t * C::kQTile);
         ok = wait1(bars->q_full, seg);
         ptx::tc_fence_after();
-        const auto scores = [&](int i) {
-          if (!wait1(bars->full[slot], slot_phase)) return false;
-          if (!split || (i & 1) == t) {
-            if (c_s >= 2 && !wait1(bars->pv_done[t][c_s & 1], (c_s - 2) >> 1)) return false;  // its weights were read
-            ptx::tc_fence_after();
-            const uint32_t kb = sbase + C::kOffPages + slot * C::kPage;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                tc_mma_f8(tile + (c_s & 1) * 64, sdesc_rows<D>(qb + h * C::kQTile + 32 * kk),
-                          sdesc_rows<D>(kb + 32 * kk), idesc_dense(kPageTokens), h != 0 || kk != 0);
-            ptx::tc_commit(bar(bars->s_full[t][c_s & 1]));
-            ptx::tc_commit(bar(bars->empty[slot]));
-            ++c_s;
-          } else {
-            ptx::mbar_arrive(bar(bars->empty[slot]));
-          }
-          if (++slot == C::kSlots) {
-            slot = 0;
-            slot_phase ^= 1;
-          }
-          return true;
-        };
-        const int ahead = split ? 2 : 1;
-        bool first = true;  // no value product in this segment yet
-        int next = 0;
-        for (int i = 0; i < pages && ok; ++i) {
-          while (ok && next < pages && next <= i + ahead) {
-            ok = scores(next++);
-            if (next == pages) ptx::tc_commit(bar(bars->q_free));
-          }
-          if (!ok || !wait1(bars->v16_full[vb], v_phase)) {
-            ok = false;
-            break;
-          }
-          if (!split || (i & 1) == t) {
-            if (first) {
-              if (seg > 0 && !wait1(bars->o_free[t], seg - 1)) {
-                ok = false;
-                break;
+        bool first = true;     // no value product in this segment yet
+        int si = 0, vi = 0;    // pages whose scores, whose value products are issued (or the other tile's)
+        uint32_t polls = 0;
+        long long since = 0;
+        while (ok && vi < pages) {
+          bool moved = false;
+          if (ready(bars->v16_full[vb], v_phase)) {
+            const bool own = !split || (vi & 1) == t;
+            if (own && ready(bars->p_full[t][c_v & 1], c_v >> 1)) {
+              if (first) {
+                if (seg > 0 && !wait1(bars->o_free[t], seg - 1)) {
+                  ok = false;
+                  break;
+                }
+                misc->nan_count[t] = 0;
               }
-              misc->nan_count[t] = 0;
-            }
-            const unsigned long long nan = misc->nan_tokens[vb];
-            if (nan != 0) {
-              const int at = misc->nan_count[t];
-              if (at < kNanPages) {
-                misc->nan_page[t][at] = k.first + i;
-                misc->nan_list[t][at] = nan;
+              const unsigned long long nan = misc->nan_tokens[vb];
+              if (nan != 0) {
+                const int at = misc->nan_count[t];
+                if (at < kNanPages) {
+                  misc->nan_page[t][at] = k.first + vi;
+                  misc->nan_list[t][at] = nan;
+                }
+                misc->nan_count[t] = at + 1;
               }
-              misc->nan_count[t] = at + 1;
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kPageTokens / 16; ++kk)
+                tc_mma_f16_ta(tile + 128, tile + (c_v & 1) * 64 + 8 * kk,
+                              ptx::sdesc_k128_sw128(sbase + C::kOffV16 + vb * C::kV16 + 32 * kk), idesc_dense(D),
+                              !first || kk != 0);
+              ptx::tc_commit(bar(bars->pv_done[t][c_v & 1]));
+              ptx::mbar_arrive(bar(bars->pv_done[t][c_v & 1]));
+              ptx::tc_commit(bar(bars->v16_empty[vb]));
+              ++c_v;
+              first = false;
+              moved = true;
+            } else if (!own) {
+              ptx::mbar_arrive(bar(bars->v16_empty[vb]));
+              moved = true;
             }
-            if (!wait1(bars->p_full[t][c_v & 1], c_v >> 1)) {
+            if (moved) {
+              ++vi;
+              if (++vb == C::kV16Bufs) {
+                vb = 0;
+                v_phase ^= 1;
+              }
+            }
+          }
+          if (si < pages && ready(bars->full[slot], slot_phase)) {
+            const bool own = !split || (si & 1) == t;
+            // (the weights that lie where the scores go were read)
+            const bool room = c_s < 2 || (c_s < c_v + 2 && ready(bars->pv_done[t][c_s & 1], (c_s - 2) >> 1));
+            if (own && room) {
+              ptx::tc_fence_after();
+              const uint32_t kb = sbase + C::kOffPages + slot * C::kPage;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                  tc_mma_f8(tile + (c_s & 1) * 64, sdesc_rows<D>(qb + h * C::kQTile + 32 * kk),
+                            sdesc_rows<D>(kb + 32 * kk), idesc_dense(kPageTokens), h != 0 || kk != 0);
+              ptx::tc_commit(bar(bars->s_full[t][c_s & 1]));
+              ptx::tc_commit(bar(bars->empty[slot]));
+              ++c_s;
+            } else if (!own) {
+              ptx::mbar_arrive(bar(bars->empty[slot]));
+            }
+            if (!own || room) {
+              ++si;
+              if (si == pages) ptx::tc_commit(bar(bars->q_free));
+              if (++slot == C::kSlots) {
+                slot = 0;
+                slot_phase ^= 1;
+              }
+              moved = true;
+            }
+          }
+          if (moved) {
+            polls = 0;
+          } else if (++polls == 1) {
+            since = clock64();
+          } else if ((polls & 63) == 0) {
+            if (*abort || clock64() - since > kWaitClocks) {
+              *abort = 1;
+              if (p.status) atomicOr(p.status, kKvErrTimeout);
               ok = false;
               break;
             }
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kPageTokens / 16; ++kk)
-              tc_mma_f16_ta(tile + 128, tile + (c_v & 1) * 64 + 8 * kk,
-                            ptx::sdesc_k128_sw128(sbase + C::kOffV16 + vb * C::kV16 + 32 * kk), idesc_dense(D),
-                            !first || kk != 0);
-            ptx::tc_commit(bar(bars->pv_done[t][c_v & 1]));
-            ptx::mbar_arrive(bar(bars->pv_done[t][c_v & 1]));
-            ptx::tc_commit(bar(bars->v16_empty[vb]));
-            ++c_v;
-            first = false;
-          } else {
-            ptx::mbar_arrive(bar(bars->v16_empty[vb]));
-          }
-          if (++vb == C::kV16Bufs) {
-            vb = 0;
-            v_phase ^= 1;
           }
         }
         if (ok && first && seg > 0) ok = wait1(bars->o_free[t], seg - 1);  // (every phase is waited for)
