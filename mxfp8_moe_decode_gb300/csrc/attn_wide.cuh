@@ -410,10 +410,11 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         int si = 0, vi = 0;    // pages whose scores, whose value products are issued (or the other tile's)
         uint32_t polls = 0;
         long long since = 0;
-        while (ok && vi < pages) {
+        while (ok && (vi < pages || si < pages)) {
           bool moved = false;
-          if (ready(bars->v16_full[vb], v_phase)) {
+          if (vi < pages && ready(bars->v16_full[vb], v_phase)) {
             const bool own = !split || (vi & 1) == t;
+            bool taken = !own;
             if (own && ready(bars->p_full[t][c_v & 1], c_v >> 1)) {
               if (first) {
                 if (seg > 0 && !wait1(bars->o_free[t], seg - 1)) {
@@ -442,12 +443,12 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
               ptx::tc_commit(bar(bars->v16_empty[vb]));
               ++c_v;
               first = false;
-              moved = true;
+              taken = true;
             } else if (!own) {
               ptx::mbar_arrive(bar(bars->v16_empty[vb]));
-              moved = true;
             }
-            if (moved) {
+            if (taken) {
+              moved = true;
               ++vi;
               if (++vb == C::kV16Bufs) {
                 vb = 0;
