@@ -483,14 +483,15 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
  *   lse = ln sum exp(scale * q . k) f32  [tokens, q_heads], if not null
  * A row that sees nothing gives 0 and -infinity. q bf16 [tokens, q_heads *
  * head_dim], rows ldq elements apart. Masked tokens never touch a row, whatever
- * their bytes (unwritten pages may hold NaN); a row whose q is not finite is
- * unspecified and touches no other. Results do not change from run to run.
+ * their bytes (unwritten pages may hold NaN); a row that sees a NaN is NaN, in
+ * the dims of that value or in all; a row whose q is not finite is unspecified
+ * and touches no other. Results do not change from run to run.
  *
  * workspace: device memory (16-byte aligned) of at least
  * MOE_ATTN_X8_WORKSPACE_BYTES (enough for every call), zero before its first
  * use; each call leaves it ready for the next. Calls that may overlap on the
- * GPU need workspaces of their own. One kernel on `stream`; no allocation, no
- * synchronisation, capture safe. Only pages that some row sees are read.
+ * GPU need workspaces of their own. One or two kernels on `stream`; no
+ * allocation, no synchronisation, capture safe. Only pages that some row sees are read.
  * Errors as moe_kv_append_x8, and MOE_ERR_ARG for a scale that is not positive
  * and finite, a negative window or sinks, max_q < 1, q_heads not a multiple of
  * kv_heads, or a workspace that is too small; MOE_ERR_UNSUPPORTED for more

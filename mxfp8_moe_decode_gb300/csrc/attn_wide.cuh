@@ -17,11 +17,13 @@
 //    down once (its thread reads and writes its TMEM lane). f16 holds 2^15, and
 //    11 bits down to 2^-21 of the reference.
 //  The page's value scale goes into P relative to the largest one so far
-//    (exact halvings); a larger one scales O down the same way.
+//    (halvings, exact while f16 holds the bits: a weight on a page whose scale
+//    is 2^-k of the largest keeps 11 bits down to 2^(k - 21) of the reference);
+//    a larger one scales O down the same way.
 //
 // Masked tokens: scores are replaced; a value byte that is NaN becomes 0 in the
-// shared tile, and the rows that see its token are made NaN at the item's end,
-// so an unwritten or masked place touches nobody.
+// shared tile, and the rows that see its token are made NaN (in all dims) at the
+// item's end, so an unwritten or masked place touches nobody.
 //
 // Per page and tile the tensor cores need 256 cycles for the scores (2 x 4
 // products of 32) and 256 for the values, the softmax about 64 x 6
@@ -47,7 +49,10 @@ namespace attn {
 
 constexpr float kLog2PWide = 7.0f;
 constexpr float kHeadroom = 8.0f;  // how far above the reference a row's scores may rise (log2)
-constexpr int kNanPages = 6;       // pages with NaN values that are listed one by one per item part
+// Pages that some rows of a group see whole or in part and others do not: its
+// positions span at most 255 tokens, so causality cuts 5 pages, the window's
+// start 5 and the sinks' end one.
+constexpr int kNanPages = 11;
 
 template <int D>
 struct WideCfg {
@@ -65,7 +70,7 @@ struct WideCfg {
   static constexpr uint32_t kOffV16 = kOffPages + kSlots * kPage;
   static constexpr uint32_t kOffBar = kOffV16 + kV16Bufs * kV16;
   static constexpr uint32_t kOffMisc = kOffBar + 512;
-  static constexpr uint32_t kOffXchg = kOffMisc + 640;   // [128 rows] {ref, sum, value scale, -}
+  static constexpr uint32_t kOffXchg = kOffMisc + 768;   // [128 rows] {ref, sum, value scale, -}
   static constexpr uint32_t kOffFactor = kOffXchg + 2048;  // [256 rows] raw score -> log2 units (keys' scale apart)
   static constexpr uint32_t kSmem = kOffFactor + 1024 + 1024;  // slack for aligning the base to 1024
   static_assert(kSmem <= 232448, "shared memory");
@@ -249,13 +254,12 @@ struct WideMisc {
   int abort;
   int id[12];                        // [slot] the page, or -1
   unsigned long long nan_tokens[3];  // [buffer] tokens with a NaN value byte
-  // [tile] this item part's pages with NaN values: page index and tokens; past
-  // the list's end its last entry covers all tokens from its page on
+  // [tile] this item part's cut pages with NaN values: page index and tokens
   int nan_count[2];
   int nan_page[2][kNanPages];
   unsigned long long nan_list[2][kNanPages];
 };
-static_assert(sizeof(WideMisc) <= 640, "misc area");
+static_assert(sizeof(WideMisc) <= 768, "misc area");
 
 template <int D>
 __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(const AttnX8Params p) {
@@ -442,10 +446,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
               const unsigned long long nan = misc->nan_tokens[vb];
               if (nan != 0) {
                 const int at = misc->nan_count[t];
-                if (at < kNanPages) {
-                  misc->nan_page[t][at] = k.first + vi;
-                  misc->nan_list[t][at] = nan;
-                }
+                misc->nan_page[t][at] = k.first + vi;
+                misc->nan_list[t][at] = nan;
                 misc->nan_count[t] = at + 1;
               }
               ptx::tc_fence_after();
@@ -597,13 +599,14 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         const int t0 = (j < walk.s.sink_pages ? j : walk.s.lo + (j - walk.s.sink_pages)) * kPageTokens;
         const int id = misc->id[slot];
         unsigned long long tokens = 0;
-        if (id >= 0 && page_kind(p, t0, t0 + kPageTokens - 1, pos_lo, pos_hi) == 1) {
+        const int kind = id < 0 ? 0 : page_kind(p, t0, t0 + kPageTokens - 1, pos_lo, pos_hi);
+        if (kind == 1) {
           values_to_f16<D, false>(src, dst, lane);
         } else {
           tokens = values_to_f16<D, true>(src, dst, lane);
           const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(tokens));
           const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(tokens >> 32));
-          tokens = id < 0 ? 0 : (static_cast<unsigned long long>(hi) << 32) | lo;
+          tokens = kind == 0 ? 0 : (static_cast<unsigned long long>(hi) << 32) | lo;
         }
         if (lane == 0) misc->nan_tokens[vb] = tokens;
         ptx::fence_proxy_async_smem();
@@ -774,12 +777,10 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           break;
         }
         const int nans = misc->nan_count[t];
-        for (int k = 0; k < min(nans, kNanPages); ++k) {
+        for (int k = 0; k < nans; ++k) {
           const int j = misc->nan_page[t][k];
           const int t0 = (j < s.sink_pages ? j : s.lo + (j - s.sink_pages)) * kPageTokens;
           if (misc->nan_list[t][k] & seen_tokens(p, t0, pos)) l = __int_as_float(0x7FC00000);
-          // (more pages than listed: whoever sees anything past this one)
-          if (k == kNanPages - 1 && nans > kNanPages && pos >= t0) l = __int_as_float(0x7FC00000);
         }
       }
       const float vscale = begun ? e8m0_value(vref) : 0.0f;

@@ -235,7 +235,7 @@ def test_append_reports_bad_pages_and_lengths():
 
 
 # ---------------------------------------------------------------- the attention
-def _check_attn(c, n, heads, window=0, sinks=0, cu=True, q=None, max_q=None, lens=None, scale=None, ws=None):
+def _check_attn(c, n, heads, window=0, sinks=0, cu=True, q=None, max_q=None, lens=None, scale=None, ws=None, tiny=0.0):
     lens = c.lens if lens is None else lens
     cu_q = np.concatenate(([0], np.cumsum(n))).tolist()
     t = cu_q[-1]
@@ -254,7 +254,7 @@ def _check_attn(c, n, heads, window=0, sinks=0, cu=True, q=None, max_q=None, len
     want, wl, spread, slack = A.attention(f64(q), A.cache_values(c.blocks, c.codes), c.table, lens, cu_q, s,
                                           window, sinks)
     got, gl = f64(out), f64(lse)
-    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread + tiny
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) - bound).max())
     empty = np.isinf(wl)
@@ -361,6 +361,93 @@ def test_attention_nan_stays_where_it_is_masked():
             b[c.table[0, t // 64], 0, kind, torch.from_numpy(image[t % 64]).to(DEV)] = 0x7F
     out, _ = M.attn_x8(q, b, codes, table, i32([200]), cu_q=i32([0, 6]), max_q=6, window=20, sinks=2)
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(7, 5), (23, 8)])  # one tile of rows, two
+@pytest.mark.parametrize("steps", [[0, 3, 6, 9, 12, 15], [15, 12, 9, 6, 3, 0], [4, 0, 9, 9, 1, 7]])
+def test_attention_many_rows_scales_that_differ_by_page(d, n, group, steps):
+    """Keys and values 2^0 .. 2^7.5 apart from page to page, in rising, falling and
+    mixed order: running maxima far above the first page's, value scales on
+    both sides of the ones before. Where every token of weight has a zero, the
+    others' e^-130 of a value is below fp32's smallest normal number, 2^-126."""
+    c = Cache([6 * PAGE - 3], 2, d, seed=sum(steps) + n)
+    grow = np.repeat(2.0 ** (np.array(steps) / 2), PAGE)[:c.lens[0], None, None]
+    k = grow * c.rng.standard_normal((c.lens[0], 2, d)) / 4
+    v = grow * c.rng.standard_normal((c.lens[0], 2, d))
+    c.blocks, c.codes = A.append(c.blocks, c.codes, A.bf16_rne(k), A.bf16_rne(v), c.table, [0], [0, c.lens[0]])
+    _check_attn(c, [n], 2 * group, tiny=2.0 ** -126)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,group", [(3, 16), (17, 8)])
+def test_attention_many_rows_of_one_long_sequence(d, n, group):
+    c = Cache([9001], 1, d, seed=n).fill()
+    ws = M.attn_x8_workspace(DEV)
+    _check_attn(c, [n], group, ws=ws)
+    _check_attn(c, [n], group, window=5000, sinks=70, ws=ws)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_ragged_batch_of_many_rows(d):
+    """Items of one and of two tiles of rows, none and many pages, in the same runs."""
+    rng = np.random.default_rng(d)
+    n = rng.integers(0, 12, 40)
+    n[::9] = rng.integers(20, 40, n[::9].size)
+    lens = rng.integers(0, 900, 40)
+    lens[5] = 0
+    c = Cache(lens.tolist(), 2, d, seed=d).fill()
+    _check_attn(c, n.tolist(), 2 * 8)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (300, 3)])
+def test_attention_many_rows_see_their_nan_only(d, window, sinks):
+    """A NaN token every 61 over many pages that causality and the window cut:
+    the rows that see one are NaN, the others keep their bits."""
+    kv, n = 700, 500
+    c = Cache([kv], 1, d, seed=12).fill()
+    blocks, codes, table = c.gpu()
+    q = torch.from_numpy(c.rng.standard_normal((n, 1, d))).bfloat16().to(DEV)
+    args = dict(cu_q=i32([0, n]), max_q=n, window=window, sinks=sinks)
+    clean, _ = M.attn_x8(q, blocks, codes, table, i32([kv]), **args)
+    key, value = A.image_bytes(d)
+    bad = list(range(330, kv, 61))
+    hit = [any(t in bad for t in A.visible(kv - n + i, kv, window, sinks)) for i in range(n)]
+    assert any(hit) and not all(hit)
+    hit = torch.tensor(hit, device=DEV)
+    for kind, image in ((0, key), (1, value)):
+        b = blocks.clone()
+        for t in bad:
+            b[c.table[0, t // PAGE], 0, kind, torch.from_numpy(image[t % PAGE]).to(DEV)] = 0x7F
+        out, _ = M.attn_x8(q, b, codes, table, i32([kv]), **args)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_many_rows_report_bad_pages_and_lengths(d):
+    c = Cache([400, 70], 1, d, seed=3).fill()
+    q = torch.from_numpy(c.rng.standard_normal((2 * 9, 4, d))).bfloat16().to(DEV)
+    blocks, codes, _ = c.gpu()
+    ws = M.attn_x8_workspace(DEV)
+
+    def call(table, lens):
+        status = i32([0])
+        out, _ = M.attn_x8(q, blocks, codes, torch.from_numpy(table).to(DEV), i32(lens), cu_q=i32([0, 9, 18]),
+                           max_q=9, workspace=ws, status=status)
+        torch.cuda.synchronize()
+        return out, status.item()
+
+    good, st = call(c.table, [400, 70])
+    assert st == 0
+    for bad in (-1, c.pages, 1 << 30):
+        t = c.table.copy()
+        t[0, 1] = bad
+        out, st = call(t, [400, 70])
+        assert st == _lib.KV_STATUS_PAGE and torch.equal(out[9:], good[9:]) and torch.isfinite(out).all()
+    out, st = call(c.table, [-4, 70])
+    assert st == _lib.KV_STATUS_LENGTH and (out[:9] == 0).all() and torch.equal(out[9:], good[9:])
 
 
 def test_attention_row_of_nan_queries_touches_no_other():
