@@ -777,6 +777,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           break;
         }
         const int nans = misc->nan_count[t];
+#pragma unroll 1
         for (int k = 0; k < nans; ++k) {
           const int j = misc->nan_page[t][k];
           const int t0 = (j < s.sink_pages ? j : s.lo + (j - s.sink_pages)) * kPageTokens;
