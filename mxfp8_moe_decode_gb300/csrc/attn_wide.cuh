@@ -25,10 +25,16 @@
 // shared tile, and the rows that see its token are made NaN (in all dims) at the
 // item's end, so an unwritten or masked place touches nobody.
 //
-// Per page and tile the tensor cores need 256 cycles for the scores (2 x 4
-// products of 32) and 256 for the values, the softmax about 64 x 6
-// instructions per row; mma.sync on the same work takes 142 cycles for every 8
-// rows on the tensor pipe and converts K and V once per 16 rows.
+// Bound by the tensor cores' operand reads. Per page and tile of D = 128 the
+// scores are 8 products of 64 x 32 and the values 4 of 128 x 16; with two
+// issuers one of the first takes 61 cycles (its 6 KB of shared-memory operands
+// at about 100 bytes a cycle; 33 by the peak rate) and one of the second 70:
+// 770 cycles, the softmax about 1000 beside it. mma.sync on the same work takes
+// 142 cycles for every 8 rows and converts K and V once per 16 rows: 238 us
+// where this takes 54 (48 query tokens over 32k, 8 heads with 5 query heads
+// each), 66 where it takes 37 (6 sequences of 8 tokens over 3k to 8k). Of the
+// 54 us about 28 are the pages (27 a CTA, 2050 cycles each), 3.5 the start, 5
+// more pass to the first scores, 4 are the output, the rest the join of 19 parts.
 //
 // Row groups of more than 128 rows fill both tiles, and every page goes to both.
 // Smaller ones have one tile of rows: its two softmax groups take the pages in
@@ -890,7 +896,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
 
 // The rows of items that several CTAs share, joined with the whole GPU behind
 // the kernel above (in it, the few CTAs that arrive last would take longer for
-// up to 256 rows than all the rest: 110 of 207 us for 240 rows in 19 parts).
+// up to 256 rows than all the rest: 110 of 207 us for 240 rows in 19 parts; here
+// 9 us by itself, 14 with one group of threads and a grid of blocks by CTA).
 // A part holds four dims of all rows after another, then each row's
 // {reference, sum}. A unit is kJoinRows rows of an item: four dims of a row per
 // thread, neighbouring lanes on neighbouring rows, the item's parts in turn to

@@ -13,7 +13,7 @@ namespace moe {
 // per warp (48 sequences over 3.5k tokens, 8 heads of 128: 94 us, where two
 // warps that share the pages take 97, and 73 against 57 for heads of 64).
 // Beyond: the tcgen05 kernel's two tiles of 128 (32 rows over 12 such
-// sequences: 46 us, by two tiles on each of two warps 55; for 16 rows it takes
+// sequences: 44 us, by two tiles on each of two warps 55; for 16 rows it takes
 // 132). Heads of 256, whose key rows are not an operand tile of it, have pages
 // shared by two or three warps: a group of 16 rows takes 51 us where one of 24
 // takes 64 (12 sequences), so the split of less work in that ratio is chosen.

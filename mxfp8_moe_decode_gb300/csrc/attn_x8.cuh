@@ -47,6 +47,16 @@
 // once per query token of the tile with the other tokens' value bytes zeroed,
 // so that a NaN in an unwritten or masked place stays there.
 //
+// Bound by HBM while a warp's work on a page (about 700 instructions per tile of
+// 8 rows) stays below its six-fold share of the page's copy time. 8 heads of
+// 128, 5 query heads each: 48 sequences of up to 16k tokens 131 us (6.3 TB/s,
+// 93 % of a plain copy's rate), up to 4k 41 us (72 %), one of 131k 48 us (82 %),
+// 16 windows of 4k 25 us (72 %). What is left is about 10 us a call: the start (3),
+// an item's end and the next one's rows (1.5 to 2 each, covered by the copies
+// that run ahead), the teams' and CTAs' joins (3 to 5). 16 rows: 94 us where 8
+// take 64 (48 sequences over 3.5k tokens), the conversions and MMAs of two
+// tiles then take longer than the copies.
+//
 #pragma once
 
 #include <cuda_fp16.h>

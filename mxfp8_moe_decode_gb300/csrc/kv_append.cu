@@ -17,6 +17,10 @@
 // none leaves. Keys are rows; values go through shared memory (16 tokens x 4
 // dims per thread, transposed with byte permutes) so that whole 16-byte
 // chunks are stored.
+// 8 heads of 128: two prompts of 4100 tokens 12.0 us (50 MB, 4.2 TB/s: 2100 CTAs
+// are 1.7 times what the SMs hold, and each is a chain of page lookup, loads,
+// maximum and stores; more resident CTAs by fewer registers took 15 to 18 us);
+// 48 sequences of one token 3.8 us, one such chain.
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"

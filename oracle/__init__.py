@@ -22,6 +22,7 @@ Modules:
 * :mod:`oracle.mx`       -- the E8M0 scale code, 32-group quantisation, and
   the dequantisation of 32 x 32-block E4M3 and per-row 1 x 32 E2M1 weights.
 * :mod:`oracle.moe`      -- RMSNorm, router, experts, combine, whole step.
+* :mod:`oracle.attention` -- residual addition, the 8-bit paged cache, attention over it.
 
 Pinning status (what fixes each function other than itself) is listed in each
 module's header. The end-to-end step composes pinned pieces; its numbers have
