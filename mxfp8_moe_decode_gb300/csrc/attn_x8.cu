@@ -9,11 +9,11 @@
 namespace moe {
 
 // Rows of a row group for `rows` query rows of one sequence and key/value head.
-// Up to 8: a warp per page, one tile of rows (attn_x8.cuh). Up to 16: two tiles
-// per warp (48 sequences over 3.5k tokens, 8 heads of 128: 94 us, where two
-// warps that share the pages take 97, and 73 against 57 for heads of 64).
-// Beyond: the tcgen05 kernel's two tiles of 128 (32 rows over 12 such
-// sequences: 44 us, by two tiles on each of two warps 55; for 16 rows it takes
+// Up to 8: a warp per page, one tile of rows (attn_x8.cuh). Up to 16: two warps
+// that share the pages (D = 128; 48 sequences over 3.5k tokens, 8 heads: 77 us,
+// two tiles on one warp 94) or two tiles on one warp (D = 64: 49 us, two warps
+// 52 to 58). Beyond: the tcgen05 kernel's two tiles of 128 (32 rows over 12 such
+// sequences: 44 us, two tiles on each of two warps 55; for 16 rows it takes
 // 132). Heads of 256, whose key rows are not an operand tile of it, have pages
 // shared by two or three warps: a group of 16 rows takes 51 us where one of 24
 // takes 64 (12 sequences), so the split of less work in that ratio is chosen.

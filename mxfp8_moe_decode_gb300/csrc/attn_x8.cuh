@@ -53,9 +53,8 @@
 // 93 % of a plain copy's rate), up to 4k 41 us (72 %), one of 131k 48 us (82 %),
 // 16 windows of 4k 25 us (72 %). What is left is about 10 us a call: the start (3),
 // an item's end and the next one's rows (1.5 to 2 each, covered by the copies
-// that run ahead), the teams' and CTAs' joins (3 to 5). 16 rows: 94 us where 8
-// take 64 (48 sequences over 3.5k tokens), the conversions and MMAs of two
-// tiles then take longer than the copies.
+// that run ahead), the teams' and CTAs' joins (3 to 5). 16 rows: 77 us where 8
+// take 64 (48 sequences over 3.5k tokens): two warps then convert each page.
 //
 #pragma once
 
@@ -76,10 +75,14 @@ constexpr int kItemCost = 10;    // starting and joining an item costs about as 
 
 template <int D, int NT, int RW>
 struct Cfg {
-  // Two slots a team at least: 12 pages of 16 KB (D = 128) for six teams; of the
-  // 32 KB pages of D = 256 six for three teams of one warp or two teams of two,
-  // four for two teams of three.
-  static constexpr int kWarps = D == 256 && RW == 1 ? 3 : D == 256 && RW == 2 ? 4 : 6;
+  // Two slots a team at least, 255 registers a thread (8 warps), and room for
+  // the teams' join: of 12 pages of 16 KB (D = 128) two for each of six warps or
+  // three for each of four teams of two (16 rows: 77 us, by six such warps 97; 48
+  // sequences over 3.5k tokens, 8 heads); of 24 pages of 8 KB (D = 64) three for
+  // each of eight warps (8 rows: 37 us, with six 42, with twelve 38); of the 32 KB
+  // pages of D = 256 six for three teams of one warp or two of two (16 rows: 102
+  // us, three of two 109), four for two teams of three.
+  static constexpr int kWarps = D == 256 ? (RW == 1 ? 3 : RW == 2 ? 4 : 6) : D == 64 || RW == 2 ? 8 : 6;
   static constexpr uint32_t kRingBytes = D == 256 && RW == 3 ? 131072 : 196608;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTeams = kWarps / RW;
