@@ -276,8 +276,10 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
   parts = 0;
   int total = 0, items = 0, longest = 0;
   bool odd_len = false;
+  Seq head = {};  // of sequence `lane`, which the search below begins with
   for (int b = lane; b < p.seqs; b += 32) {
     const Seq s = load_seq<kRows>(p, b);
+    if (b == lane) head = s;
     odd_len |= __ldg(p.kv_len + b) != s.kv;
     const int n = s.groups * p.kv_heads;
     total += item_size(s) * n;
@@ -305,8 +307,11 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
   if (at >= (parts ? items : total)) return false;
   int base = 0, seen = 0;  // list position and units before the current 32 sequences
   for (int b0 = 0;; b0 += 32) {
-    Seq s = {};
-    if (b0 + lane < p.seqs) s = load_seq<kRows>(p, b0 + lane);
+    Seq s = head;
+    if (b0 > 0) {
+      s = {};
+      if (b0 + lane < p.seqs) s = load_seq<kRows>(p, b0 + lane);
+    }
     const int n = s.groups * p.kv_heads, size = item_size(s) * n, step = parts ? n : size;
     if (b0 + 32 < p.seqs) {
       const int all = __reduce_add_sync(0xffffffffu, step);
