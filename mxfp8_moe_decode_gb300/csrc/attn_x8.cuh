@@ -274,7 +274,7 @@ template <int kRows, int kUneven>
 __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int lane, int warp, Walk& walk,
                                          int& per, int& parts) {
   parts = 0;
-  int total = 0, items = 0, longest = 0;
+  int total = 0, items = 0, longest = 0, tokens = 0;
   bool odd_len = false;
   Seq head = {};  // of sequence `lane`, which the search below begins with
   for (int b = lane; b < p.seqs; b += 32) {
@@ -285,12 +285,16 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
     total += item_size(s) * n;
     items += n;
     longest = max(longest, s.pages);
+    tokens = min(tokens + s.n, 1 << 25);  // (32 lanes' fit 32 bits)
   }
+  // Starts that do not ascend: the list could be longer than 32 bits count.
+  const bool disorder = static_cast<int>(__reduce_add_sync(0xffffffffu, tokens)) > p.tokens;
+  odd_len |= disorder;
   if (odd_len && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, kKvErrLength);
   total = __reduce_add_sync(0xffffffffu, total);
   items = __reduce_add_sync(0xffffffffu, items);
   longest = __reduce_max_sync(0xffffffffu, longest);
-  if (items == 0) return false;
+  if (items == 0 || disorder) return false;
   const int cta = blockIdx.x, grid = gridDim.x;
   per = div_pos(total + grid - 1, grid);
   // Aligned: every item in `parts` equal parts, when that makes no run longer

@@ -508,6 +508,26 @@ def test_attention_reports_bad_pages_and_lengths():
     assert (st, st2) == (0, _lib.KV_STATUS_LENGTH) and torch.equal(out, good)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("max_q", [1, 8, 40])
+def test_attention_refuses_row_starts_that_do_not_ascend(d, max_q):
+    c = Cache([100, 100, 100], 1, d, seed=2).fill()
+    q = torch.ones(8, 2, d, dtype=torch.bfloat16, device=DEV)
+    blocks, codes, table = c.gpu()
+    ws = M.attn_x8_workspace(DEV)
+    out = torch.full_like(q, 5.0)
+    status = i32([0])
+    M.attn_x8(q, blocks, codes, table, i32(c.lens), cu_q=i32([0, 6, 2, 8]), max_q=max_q, out=out, workspace=ws,
+              status=status)
+    torch.cuda.synchronize()
+    assert status.item() == _lib.KV_STATUS_LENGTH and (out == 5).all()
+    status.zero_()
+    M.attn_x8(q, blocks, codes, table, i32(c.lens), cu_q=i32([0, 6, 6, 8]), max_q=max_q, out=out, workspace=ws,
+              status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and torch.isfinite(out).all() and not (out == 5).all()
+
+
 def test_append_then_attention_in_a_graph():
     """A decode step captured once and replayed as the sequences grow."""
     d, kvh, heads = 128, 2, 10
