@@ -265,8 +265,8 @@ __device__ __forceinline__ bool next_segment(const AttnX8Params& p, Walk& k) {
 
 // This CTA's run of the work list, found by every warp for itself, 32 sequences
 // at a time (nothing to wait for but the lengths): once over them for the
-// list's length, once more to the run's start. False: nothing to do (the same
-// in every warp). `teams`: pages that a CTA works on at once. parts: CTAs per
+// list's length, once more (the first 32 from registers) to the run's start.
+// False: nothing to do (the same in every warp). `teams`: pages that a CTA works on at once. parts: CTAs per
 // item (aligned runs), or 0 and then per: list positions per run. kUneven: how
 // much longer than others a run may be, in eighths (bandwidth goes where pages
 // are left, the time of products does not).
