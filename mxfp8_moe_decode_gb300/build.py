@@ -1,8 +1,11 @@
-"""Builds libmoe_decode.so (the CUDA kernels + the C ABI) in-tree with nvcc.
+"""Builds libmoe_decode.so (the CUDA kernels + the C ABI) in-tree with nvcc, and
+the Python module _host.so (argument marshalling on torch tensors) with g++.
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared library with the CUDA runtime linked statically (the library
 loads without a GPU; the driver is reached through the runtime at first use).
+_host.so is built against the torch that is installed and gets the library's
+entry points by address.
 """
 
 from __future__ import annotations
@@ -10,12 +13,14 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_decode.so")
+HOST = os.path.join(HERE, "_host.so")
 SOURCES = ["api.cu", "seam.cu", "router.cu", "scales.cu", "expert.cu", "combine.cu",
            "route_static.cu", "attn_seam.cu", "add_norm.cu", "kv_append.cu", "attn_x8.cu",
            "attn_x8_d64.cu", "attn_x8_d128.cu", "attn_x8_d256.cu"]
@@ -40,10 +45,28 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _build_host() -> None:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = HOST + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{root}/include",
+           f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           os.path.join(CSRC, "host.cpp"), "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on host.cpp:\n{r.stderr}")
+    os.replace(tmp, HOST)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOST):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "moe_decode.h"))
     deps.append(os.path.abspath(__file__))
@@ -56,8 +79,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = ex.submit(_build_host)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

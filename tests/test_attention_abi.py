@@ -33,13 +33,6 @@ def test_constants_match_the_header():
         assert int(val["MOE_KV_STATUS_" + bit]) == getattr(_lib, "KV_STATUS_" + bit)
 
 
-def test_packed_structs_are_the_headers():
-    from mxfp8_moe_decode_gb300 import attention as A
-    cache, seqs = (1, 2, 3, 4, 5), (1, 2, 3, 4, 5, 6, 7)
-    assert bytes(KvCache(*cache))[:A._CACHE.size] == A._CACHE.pack(*cache)
-    assert bytes(KvSeqs(*seqs))[:A._SEQS.size] == A._SEQS.pack(*seqs)
-
-
 def test_add_norm_refusals(L):
     def call(x=P[0], ldx=256, r=P[1], ldr=256, w=P[2], m=4, h=256, eps=1e-6, res=P[3], x8=P[4],
              c=P[5], n=P[6]):

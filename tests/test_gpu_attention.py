@@ -528,6 +528,48 @@ def test_attention_refuses_row_starts_that_do_not_ascend(d, max_q):
     assert status.item() == 0 and torch.isfinite(out).all() and not (out == 5).all()
 
 
+def test_bindings_refuse_wrong_tensors():
+    """Wrong types, shapes, devices and strides, one argument at a time."""
+    d = 64
+    x = torch.zeros(3, 96, dtype=torch.bfloat16, device=DEV)
+    norm = dict(x=x, residual=x.clone(), norm_w=x[0].clone(), res_out=x.clone(),
+                x8=torch.zeros(3, 96, dtype=torch.uint8, device=DEV),
+                codes=torch.zeros(3, 3, dtype=torch.uint8, device=DEV), normed=x.clone())
+    blocks, codes = M.kv_cache_x8(2, 2, d, DEV)
+    k = torch.zeros(2, 2, d, dtype=torch.bfloat16, device=DEV)
+    seqs = dict(page_table=i32([[0], [1]]), cu_q=i32([0, 1, 2]), status=i32([0]))
+    append = dict(blocks=blocks, codes=codes, k=k, v=k.clone(), start=i32([0, 0]), **seqs)
+    attn = dict(q=torch.zeros(2, 4, d, dtype=torch.bfloat16, device=DEV), blocks=blocks, codes=codes, kv_len=i32([1, 1]),
+                out=torch.zeros(2, 4, d, dtype=torch.bfloat16, device=DEV),
+                lse=torch.zeros(2, 4, device=DEV), workspace=M.attn_x8_workspace(DEV), **seqs)
+    for fn, args in ((M.add_norm_x8, norm), (M.kv_append_x8, append), (M.attn_x8, attn)):
+        fn(**args)
+        for name, t in args.items():
+            bad = [t.cpu(), t.unsqueeze(0), 5]
+            if name != "workspace":  # (any type, any shape)
+                bad += [t.double(), t.flatten()[:-1]]
+            if t.dim() > 1:
+                bad.append(t.transpose(-1, -2).contiguous().transpose(-1, -2))
+            for b in bad[:-2] if name == "workspace" else bad:
+                if isinstance(b, torch.Tensor) and b.shape == t.shape and b.stride() == t.stride() \
+                        and b.dtype == t.dtype and b.device == t.device:
+                    continue  # (one column: still contiguous)
+                with pytest.raises(ValueError):
+                    fn(**{**args, name: b})
+    for name, b in (("max_q", 2 ** 40), ("window", 2 ** 31), ("sinks", -2 ** 40)):
+        with pytest.raises(ValueError):
+            M.attn_x8(**{**attn, name: b})
+    with pytest.raises(_lib.MoeError):
+        M.attn_x8(**{**attn, "window": -1})
+    with pytest.raises(_lib.MoeError):
+        M.attn_x8(**{**attn, "workspace": attn["workspace"][:4096]})
+    with pytest.raises(TypeError):
+        M.attn_x8(**{**attn, "scale": "1"})
+    with pytest.raises(ValueError):
+        M.kv_append_x8(**{**append, "cu_q": None, "page_table": i32([[0]]), "start": i32([0])})
+    torch.cuda.synchronize()
+
+
 def test_append_then_attention_in_a_graph():
     """A decode step captured once and replayed as the sequences grow."""
     d, kvh, heads = 128, 2, 10
