@@ -17,10 +17,11 @@
 // none leaves. Keys are rows; values go through shared memory (16 tokens x 4
 // dims per thread, transposed with byte permutes) so that whole 16-byte
 // chunks are stored.
-// 8 heads of 128: two prompts of 4100 tokens 12.0 us (50 MB, 4.2 TB/s: 2100 CTAs
+// 8 heads of 128: two prompts of 4100 tokens 10.7 us (50 MB, 4.7 TB/s: 2100 CTAs
 // are 1.7 times what the SMs hold, and each is a chain of page lookup, loads,
 // maximum and stores; more resident CTAs by fewer registers took 15 to 18 us);
-// 48 sequences of one token 3.8 us, one such chain.
+// 48 sequences of one token 3.5 us, one such chain. The values' CTAs, which do
+// more, come first in the grid (the keys' first: 11.4 us).
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   __shared__ __align__(16) uint8_t stage[kPageTokens * kPitch];
   __shared__ uint32_t red[2][kThreads / 32];
   const int tid = threadIdx.x;
-  const int head = blockIdx.y, kv = blockIdx.z;
+  const int head = blockIdx.y, kv = 1 - blockIdx.z;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
@@ -219,9 +220,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     d[1] = q.y;
   }
   __syncthreads();
-  // unit = (16-token chunk, 4 dims): 16 words in, four 16-byte chunks out
+  // unit = (16-token chunk, 4 dims): 16 words in, four 16-byte chunks out; four
+  // neighbouring lanes store a whole row (the chunks of one number: 0.5 us more)
   for (int u = tid; u < 4 * (D / 4); u += kThreads) {
-    const int ch = u / (D / 4), d0 = (u % (D / 4)) * 4;
+    const int ch = u & 3, d0 = (u >> 2) * 4;
     const int lo = ch * 16, hi = lo + 16;
     if (hi <= off || lo >= off + count) continue;
     const bool whole = lo >= off && hi <= off + count;
