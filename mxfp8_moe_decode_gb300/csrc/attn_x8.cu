@@ -95,7 +95,9 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   p.group = group;
   p.group_magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(group) + 1);
   p.max_kv = seqs->max_pages * kPageTokens;
-  p.window = window;
+  // A window as long as the longest sequence hides nothing, and one below that
+  // keeps position - window in 32 bits for rows before the first token too.
+  p.window = window < p.max_kv ? window : 0;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

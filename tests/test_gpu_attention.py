@@ -293,6 +293,21 @@ def test_attention_window_and_sinks(window, sinks, n):
     _check_attn(c, n, 2, window, sinks)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30, 192, 191])
+@pytest.mark.parametrize("n,lens", [([8], [1]), ([7, 10, 1], [5, 3, 150]), ([40, 30], [33, 2])])
+def test_attention_window_beyond_every_length(n, lens, window, d):
+    """Windows up to the largest int with rows before the first token: position -
+    window stays in range, and the rows that see tokens see all of them."""
+    c = Cache(lens, 1, d, seed=len(n), extra_width=3 - max(-(-max(lens) // PAGE), 1)).fill()
+    assert c.table.shape[1] == 3  # 192 tokens at most
+    for heads in (1, 3):  # (by the rows per key/value head: few, shared pages, many)
+        q = torch.from_numpy(c.rng.standard_normal((sum(n), heads, d))).bfloat16().to(DEV)
+        plain, _ = _check_attn(c, n, heads, q=q)
+        out, _ = _check_attn(c, n, heads, window, 2, q=q)
+        assert torch.equal(out, plain)
+
+
 def test_attention_one_long_sequence_over_all_ctas():
     c = Cache([20000], 1, 64, seed=5).fill()
     ws = M.attn_x8_workspace(DEV)
