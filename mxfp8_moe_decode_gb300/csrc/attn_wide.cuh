@@ -77,8 +77,13 @@ struct WideCfg {
   static constexpr uint32_t kOffBar = kOffV16 + kV16Bufs * kV16;
   static constexpr uint32_t kOffMisc = kOffBar + 512;
   static constexpr uint32_t kOffXchg = kOffMisc + 768;   // [128 rows] {ref, sum, value scale, -}
-  static constexpr uint32_t kOffFactor = kOffXchg + 2048;  // [256 rows] raw score -> log2 units (keys' scale apart)
-  static constexpr uint32_t kSmem = kOffFactor + 1024 + 1024;  // slack for aligning the base to 1024
+  // [segment & 1][256 rows] raw score -> log2 units (keys' scale apart). Two
+  // buffers: a segment's rows may be made while a softmax warp has yet to read
+  // its factor of the one before (q_free follows the score products alone), but
+  // not before every softmax warp made the rows of that one, which it does
+  // behind its read of the factor two before.
+  static constexpr uint32_t kOffFactor = kOffXchg + 2048;
+  static constexpr uint32_t kSmem = kOffFactor + 2048 + 1024;  // slack for aligning the base to 1024
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
     constexpr int kPer = 8, kChunks = D / 32, kMakers = 8 + C::kConverters, kBatch = 2;
     const int sub = lane >> 2, l4 = lane & 3;
     const int rows = k.s.n * p.group, row0 = k.group * C::kRows, count = min(rows - row0, C::kRows);
-    float* factors = reinterpret_cast<float*>(smem + C::kOffFactor);
+    float* factors = reinterpret_cast<float*>(smem + C::kOffFactor) + (seg & 1) * C::kRows;
     const __nv_bfloat16* base = p.q + k.s.q0 * p.ldq + static_cast<long long>(k.head * p.group) * D + l4 * 8;
     for (int i0 = who * kPer; i0 < count; i0 += kBatch * kMakers * kPer) {
       uint4 v[kBatch][kChunks];
@@ -671,7 +676,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         ok = false;
         break;
       }
-      const float factor = r < rows ? reinterpret_cast<const float*>(smem + C::kOffFactor)[lr] : 0.0f;
+      const float factor =
+          r < rows ? reinterpret_cast<const float*>(smem + C::kOffFactor)[(seg & 1) * C::kRows + lr] : 0.0f;
 
       float ref = -INFINITY, l = 0.0f;
       int vref = 0;       // the value code that P is relative to

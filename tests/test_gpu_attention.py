@@ -415,6 +415,20 @@ def test_attention_ragged_batch_of_many_rows(d):
     _check_attn(c, n.tolist(), 2 * 8)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [3, 8])
+def test_attention_short_items_of_rows_of_other_sizes(group, d):
+    """400 items of one to three pages, several in turn on a CTA, the rows of
+    neighbours 2^20 apart: an item scaled by another's factors shows."""
+    rng = np.random.default_rng(group)
+    n = rng.integers(24 // group, 24 // group + 5, 200)
+    lens = np.maximum(rng.integers(1, 190, 200), n)
+    c = Cache(lens.tolist(), 2, d, seed=d).fill()
+    amp = np.repeat(2.0 ** (10 * (np.arange(200) % 3 - 1)), n)[:, None, None]
+    q = torch.from_numpy(amp * c.rng.standard_normal((n.sum(), 2 * group, d))).bfloat16().to(DEV)
+    _check_attn(c, n.tolist(), 2 * group, q=q, scale=2.0 ** -10 * d ** -0.5)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (300, 3)])
 def test_attention_many_rows_see_their_nan_only(d, window, sinks):
