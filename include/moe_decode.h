@@ -430,7 +430,8 @@ typedef struct moe_kv_cache {
  *  tokens                        rows of the call (0 enqueues nothing)
  *  max_q                         (attention, with cu_q) the largest number of
  *                                tokens of one sequence: a kernel is chosen by
- *                                it, results do not depend on it
+ *                                it, and with it the roundings (moe_attn_x8
+ *                                names both kernels'), not what a row sees
  */
 typedef struct moe_kv_seqs {
   const int32_t* page_table;
@@ -487,6 +488,17 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
  * their bytes (unwritten pages may hold NaN); a row that sees a NaN is NaN, in
  * the dims of that value or in all; a row whose q is not finite is unspecified
  * and touches no other. Results do not change from run to run.
+ *
+ * Scores, softmax statistics and sums are fp32. Rounded below that: the weights
+ * in front of the values are f16, and q is scaled per row to what the tensor
+ * cores take.
+ *  up to 16 rows (max_q * q_heads / kv_heads), and any with head_dim 256:
+ *    weights of 11 bits down to 2^-28 of the row's largest, 0 below 2^-39; q
+ *    exact down to 2^-28 of the row's largest value
+ *  more rows: weights of 11 bits down to 2^-21 of the row's largest (2^(k - 21)
+ *    on a page whose values' scale is 2^-k, k up to 8, of an earlier page's),
+ *    0 below 2^-32; q off by at most 2^-18 of the row's largest value; pages
+ *    2^80 and more quieter than what the row has summed so far may lose bits
  *
  * workspace: device memory (16-byte aligned) of at least
  * MOE_ATTN_X8_WORKSPACE_BYTES (enough for every call), zero before its first

@@ -16,10 +16,13 @@
 //    2^8 of it nothing is rescaled; beyond that, the row's O and sum are scaled
 //    down once (its thread reads and writes its TMEM lane). f16 holds 2^15, and
 //    11 bits down to 2^-21 of the reference.
-//  The page's value scale goes into P relative to the largest one so far
-//    (halvings, exact while f16 holds the bits: a weight on a page whose scale
-//    is 2^-k of the largest keeps 11 bits down to 2^(k - 21) of the reference);
-//    a larger one scales O down the same way.
+//  The page's value scale goes into P relative to one that each row keeps: that
+//    of the last page that was louder, or more than 2^8 quieter, than the one
+//    before it; O is scaled to it in the same way, down or up, as far as fp32
+//    holds the sum so far. P's halvings are exact while f16 holds the bits: a
+//    weight on a page 2^-k as loud (k <= 8) keeps 11 bits down to 2^(k - 21) of
+//    the reference. Pages of which a row sees nothing, or gives all tokens less
+//    weight than f16 holds, do not count: a scale there touches no row.
 //
 // Masked tokens: scores are replaced; a value byte that is NaN becomes 0 in the
 // shared tile, and the rows that see its token are made NaN (in all dims) at the
@@ -55,6 +58,8 @@ namespace attn {
 
 constexpr float kLog2PWide = 7.0f;
 constexpr float kHeadroom = 8.0f;  // how far above the reference a row's scores may rise (log2)
+constexpr float kNothing = 33.0f;  // below the reference by more: weights under 2^(7 - 33), 0 in f16
+constexpr int kQuieter = 8;        // value codes by which P is scaled down before O is scaled up instead
 // Pages that some rows of a group see whole or in part and others do not: its
 // positions span at most 255 tokens, so causality cuts 5 pages, the window's
 // start 5 and the sinks' end one.
@@ -680,8 +685,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           r < rows ? reinterpret_cast<const float*>(smem + C::kOffFactor)[(seg & 1) * C::kRows + lr] : 0.0f;
 
       float ref = -INFINITY, l = 0.0f;
-      int vref = 0;       // the value code that P is relative to
-      bool begun = false; // some page of this warp's rows was not all masked
+      int vref = -1;      // the value code that the row's P and O are relative to (-1: O is 0)
+      float most = 0.0f;  // a bound: |O| <= 448 most
       int own = 0;        // pages of this segment taken
       for (int i = 0; i < pages; ++i) {
         if (i > 0 && (i & 31) == 0) codes32 = page_codes(page_id(walk.first + i + lane));
@@ -717,37 +722,46 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           const float f = fmaxf(factor * e8m0_value(codes & 0xFF), FLT_MIN);  // (never 0: masked scores are -inf)
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
           const int vc = codes >> 8;
-          if (!begun) {
-            vref = vc;
-            begun = true;
-          }
           const bool rise = ref != -INFINITY && top > ref + kHeadroom;
-          if (vc > vref || __any_sync(0xffffffffu, rise)) {
+          const bool counts = top != -INFINITY && (rise || ref == -INFINITY || top >= ref - kNothing);
+          const bool turn = counts && vref >= 0 && (vc > vref || vc < vref - kQuieter);
+          if (counts && vref < 0) vref = vc;
+          if (__any_sync(0xffffffffu, rise || turn)) {
             // scale O (stable: the last own page's product is done, this one's
-            // not begun) and the sum down to the new reference
+            // not begun) and the sum down to the new reference, O to the new
+            // value scale (up by what keeps 448 most below 2^111)
             const float w = rise ? ex2(ref - top) : 1.0f;
+            int to = vref;
+            if (turn) {
+              const int room = 228 - static_cast<int>(__float_as_uint(most * w) >> 23);
+              to = vc > vref ? vc : max(vc, vref - max(room, 0));
+            }
+            // (in two factors: 2^(vref - to) may pass fp32's exponents)
+            const int by = min(max(vref - to, -126), 126);
+            const float w0 = w * __uint_as_float(static_cast<uint32_t>(127 + by) << 23);
+            const float w1 = __uint_as_float(static_cast<uint32_t>(max(127 + vref - to - by, 0)) << 23);
             if (own > 0) {
               if (!wait(bars->pv_done[t][(c - 1) & 1], (c - 1) >> 1)) {
                 ok = false;
                 break;
               }
               ptx::tc_fence_after();
-              const float wo = vc > vref ? w * ex2(static_cast<float>(vref - vc)) : w;
 #pragma unroll 1
               for (int d = 0; d < D; d += 32) {
                 uint32_t x[32];
                 tmem_ld_x32(o_cols + d, x);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * wo);
+                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * w0 * w1);
                 tmem_st_x16(o_cols + d, x);
                 tmem_st_x16(o_cols + d + 16, x + 16);
               }
               tmem_wait_st();
             }
             l *= w;
+            most = most * w0 * w1;
             if (rise) ref = top;
-            vref = max(vref, vc);
+            vref = to;
           }
           if (ref == -INFINITY) ref = top;  // the row's first visible tokens
           const float shift = kLog2PWide - (ref == -INFINITY ? 0.0f : ref);
@@ -760,12 +774,15 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
             sum[(2 * k + 1) & 3] += b;
             pk[k] = pack_f16(a, b);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (vc != vref) {
-            const __half2 dv = __float2half2_rn(ex2(static_cast<float>(vc - vref)));
+          const float page = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += page;
+          const float dv = counts && vc != vref ? ex2(static_cast<float>(vc - vref)) : 1.0f;
+          most = fmaf(page, dv, most);
+          if (dv != 1.0f) {
+            const __half2 dv2 = __float2half2_rn(dv);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pk[k]), dv);
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&pk[k]), dv2);
               pk[k] = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
@@ -796,7 +813,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           if (misc->nan_list[t][k] & seen_tokens(p, t0, pos)) l = __int_as_float(0x7FC00000);
         }
       }
-      const float vscale = begun ? e8m0_value(vref) : 0.0f;
+      const float vscale = vref < 0 ? 0.0f : e8m0_value(vref);
       const bool whole = walk.first == 0 && walk.last == s.pages;
       if (split && t == 1) {
         // tile 0's threads read this one's O and finish the rows

@@ -394,6 +394,91 @@ def test_attention_many_rows_scales_that_differ_by_page(d, n, group, steps):
     _check_attn(c, [n], 2 * group, tiny=2.0 ** -126)
 
 
+def _check_long_runs(c, n, heads, q, window=0, scale=None):
+    """c's one sequence as it is (its pages spread over the CTAs), and so many
+    times in one call that a CTA walks many pages of an item: each copy against
+    the oracle. Returns the copies' rows."""
+    s = c.d ** -0.5 if scale is None else scale
+    want, _, spread, slack = A.attention(f64(q), A.cache_values(c.blocks, c.codes), c.table, c.lens, [0, n], s, window)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread + 2.0 ** -126
+    blocks, codes, table = c.gpu()
+    most = -(-300 // c.kvh)
+    for times in (1, most):
+        out, _ = M.attn_x8(q.to(DEV).repeat(times, 1, 1), blocks, codes, table.repeat(times, 1), i32(c.lens * times),
+                           cu_q=i32([n * i for i in range(times + 1)]), max_q=n, window=window, scale=scale)
+        out = out.view(times, n, heads, c.d)
+        excess = (out.double() - torch.from_numpy(want).to(DEV)).abs() - torch.from_numpy(bound).to(DEV)
+        assert (excess <= 0).all(), excess.max().item()
+    return out
+
+
+def _paged_values(c, steps, dims, d, loud_key=None):
+    """Fills c's one sequence: values of page i times 2^steps[i], where steps[i] is
+    not 0 in the first `dims` dims only (0 elsewhere: what the quiet pages hold
+    there is all there is). loud_key: dim 0 of the keys of pages with steps[i] > 0."""
+    e = np.array(steps)[np.arange(c.lens[0]) // PAGE]
+    k = c.rng.standard_normal((e.size, c.kvh, d)) / 2
+    v = c.rng.standard_normal((e.size, c.kvh, d)) * 2.0 ** e[:, None, None]
+    v[e != 0, :, dims:] = 0.0
+    if loud_key is not None:
+        k[e > 0, :, 0] = loud_key
+    c.blocks, c.codes = A.append(c.blocks, c.codes, A.bf16_rne(k), A.bf16_rne(v), c.table, [0], [0, c.lens[0]])
+
+
+LOUD = [[60, 0, 0, 0, 0, 0], [0, 0, 60, 0, 0, 0], [0, 0, 0, 0, 0, 60], [60, 0, 60, 0, 60, 0],
+        [0, -60, 0, -60, 60, 0], [0, 20, 40, 60, 40, 0], [0, 12, 0, 9, 0, 25], [8, 0, 4, 0, 8, 1]]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,group", [(3, 1), (7, 5), (23, 8)])  # few rows, one tile, two
+@pytest.mark.parametrize("steps", LOUD)
+def test_attention_loud_pages_keep_the_others(steps, n, group, d):
+    """Pages up to 2^60 louder than the others (2^120 between two), with values in
+    8 dims: in all other dims the quiet pages' values are the whole answer."""
+    c = Cache([6 * PAGE - 3], 2, d, seed=len(steps) + n)
+    _paged_values(c, steps, 8, d)
+    _check_long_runs(c, n, 2 * group, torch.from_numpy(c.rng.standard_normal((n, 2 * group, d))).bfloat16())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,group", [(3, 1), (7, 5), (23, 8)])
+@pytest.mark.parametrize("loud", [30, 110])
+@pytest.mark.parametrize("at", [0, 2, 5])
+def test_attention_loud_pages_without_weight(at, loud, n, group, d):
+    """A page 2^30 or 2^110 louder whose scores lie some 290 log2 units below the others':
+    its share is nothing, and so is its trace."""
+    c = Cache([6 * PAGE - 3], 2, d, seed=at + n)
+    steps = [0] * 6
+    steps[at] = loud
+    _paged_values(c, steps, 8, d, loud_key=-448.0)
+    q = torch.from_numpy(c.rng.standard_normal((n, 2 * group, d)) / 2).bfloat16()
+    q[..., 0] = 3.0
+    _check_long_runs(c, n, 2 * group, q, scale=0.15)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("loud", [30, 110])
+def test_attention_loud_pages_behind_the_mask(loud, group, d):
+    """A loud page before the window of some rows and in that of others, and a loud
+    page that only the last rows are past: rows that mask it keep their bits."""
+    kv, n, window = 6 * PAGE - 10, 120, 160
+    c = Cache([kv], 1, d, seed=group)
+    steps = [0] * 6
+    steps[1] = steps[5] = loud
+    _paged_values(c, steps, d, d)
+    q = torch.from_numpy(c.rng.standard_normal((n, group, d))).bfloat16()
+    out = _check_long_runs(c, n, group, q, window)
+    quiet = Cache([kv], 1, d, seed=group)
+    _paged_values(quiet, steps, d, d)
+    quiet.codes[quiet.table[0, [1, 5]], 0, 1] -= loud
+    same = _check_long_runs(quiet, n, group, q, window)
+    pos = kv - n + np.arange(n)
+    masks = torch.from_numpy((pos - window + 1 >= 2 * PAGE) & (pos < 5 * PAGE))
+    assert 0 < masks.sum() < n
+    assert torch.equal(out[:, masks], same[:, masks])
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("n,group", [(3, 16), (17, 8)])
 def test_attention_many_rows_of_one_long_sequence(d, n, group):
