@@ -489,9 +489,10 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
  * the dims of that value or in all; a row whose q is not finite is unspecified
  * and touches no other. Results do not change from run to run.
  *
- * Scores, softmax statistics and sums are fp32. Rounded below that: the weights
- * in front of the values are f16, and q is scaled per row to what the tensor
- * cores take.
+ * Scores, softmax statistics and sums are fp32 (the sums' weights relative to
+ * the row's largest: the tokens that weigh, times |v|, stay below 2^128). Below
+ * that, the weights in front of the values are f16, and q is scaled per row to
+ * what the tensor cores take.
  *  up to 16 rows (max_q * q_heads / kv_heads), and any with head_dim 256:
  *    weights of 11 bits down to 2^-28 of the row's largest, 0 below 2^-39; q
  *    exact down to 2^-28 of the row's largest value

@@ -57,6 +57,7 @@ namespace moe {
 namespace attn {
 
 constexpr float kLog2PWide = 7.0f;
+constexpr float kUnPWide = 0x1p-15f;  // of O read out: P's scale, and the headroom, which fp32 has not for the largest values
 constexpr float kHeadroom = 8.0f;  // how far above the reference a row's scores may rise (log2)
 constexpr float kNothing = 33.0f;  // below the reference by more: weights under 2^(7 - 33), 0 in f16
 constexpr int kQuieter = 8;        // value codes by which P is scaled down before O is scaled up instead
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           if (misc->nan_list[t][k] & seen_tokens(p, t0, pos)) l = __int_as_float(0x7FC00000);
         }
       }
-      const float vscale = vref < 0 ? 0.0f : e8m0_value(vref);
+      const float vscale = vref < 0 ? 0.0f : e8m0_value(vref) * kUnPWide;
       const bool whole = walk.first == 0 && walk.last == s.pages;
       if (split && t == 1) {
         // tile 0's threads read this one's O and finish the rows
@@ -863,11 +864,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
       const int token = by_group(p, r);
       const size_t at_out = static_cast<size_t>(s.q0 + token) * (p.kv_heads * p.group) +
                             walk.head * p.group + r - token * p.group;
-      if (whole) {
-        const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-        wa *= inv;
-        wb *= inv;
-      }
+      // (behind the value scale: the two together may leave fp32's exponents)
+      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : __frcp_rn(l) * (1.0f / kUnPWide);
 #pragma unroll 2
       for (int d = 0; d < D; d += 16) {
         float x[16], y[16];
@@ -878,6 +876,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         for (int k = 0; k < 16; ++k) {
           x[k] *= wa;
           if (both) x[k] = fmaf(y[k], wb, x[k]);
+          x[k] *= inv;
         }
         if (r < rows) {
           if (whole) {
@@ -1016,7 +1015,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_wide_join_kernel(const Attn
         sum.z = fmaf(y.z, w, sum.z * keep);
         sum.w = fmaf(y.w, w, sum.w * keep);
       }
-      store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, kLog2PWide);
+      store_row<D>(p, x.q0, x.head, x.row0 + lr, d4, sum, top, den, kLog2PWide, 1.0f / kUnPWide);
     }
   }
 }

@@ -39,8 +39,8 @@
 //    it lies; P^T gets from the accumulators' layout to the B operand's by
 //    movmatrix.
 //  A page's product starts from zero and joins the running sum as
-//    O = O * alpha + acc * 2^(code - 127): one FMA per value does both the
-//    softmax's rescaling and the page's own value scale.
+//    O = O * alpha + acc * 2^(code - 127 - 14): one FMA per value does the
+//    softmax's rescaling, the page's own value scale and P's.
 //
 // Masked tokens never touch a row, whatever their bytes: scores are replaced
 // (not added to), and on pages where some row's mask cuts, the product runs
@@ -70,7 +70,8 @@
 namespace moe {
 namespace attn {
 
-constexpr float kLog2P = 14.0f;  // P is held times 2^14
+constexpr float kLog2P = 14.0f;  // P and its sum are held times 2^14
+constexpr float kUnP = 0x1p-14f;  // O is not: it has fp32's whole range for values as large as bf16's
 constexpr int kItemCost = 10;    // starting and joining an item costs about as much as its pages
 
 template <int D, int NT, int RW>
@@ -394,13 +395,14 @@ __device__ __forceinline__ int page_kind(const AttnX8Params& p, int t0, int t1, 
 }
 
 // Four dims of a finished row: sum / den, and with the first ones the lse;
-// sum and den are held times 2^log2_scale relative to `top` (log2 units).
+// both are relative to `top` (log2 units), den is held times 2^log2_scale and
+// `ratio` times as large as sum.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnX8Params& p, int q0, int head, int r, int d4, const float4& sum,
-                                          float top, float den, float log2_scale) {
+                                          float top, float den, float log2_scale, float ratio) {
   const int token = by_group(p, r);
   const size_t at = static_cast<size_t>(q0 + token) * (p.kv_heads * p.group) + head * p.group + r - token * p.group;
-  const float inv = den == 0.0f ? 0.0f : __frcp_rn(den);
+  const float inv = den == 0.0f ? 0.0f : __frcp_rn(den) * ratio;
   __align__(8) __nv_bfloat162 y[2] = {__floats2bfloat162_rn(sum.x * inv, sum.y * inv),
                                       __floats2bfloat162_rn(sum.z * inv, sum.w * inv)};
   *reinterpret_cast<uint2*>(p.out + at * D + d4 * 4) = *reinterpret_cast<const uint2*>(y);
@@ -416,7 +418,7 @@ __device__ __forceinline__ void store_row(const AttnX8Params& p, int q0, int hea
 // rows.
 template <int D, int kRows, int kWarps>
 __device__ __forceinline__ void join_shared(const AttnX8Params& p, Shared* shared, uint8_t* space, int tid,
-                                            float log2_scale) {
+                                            float log2_scale, float ratio) {
   if (shared[0].c1 < 0 && shared[1].c1 < 0) return;  // (the same in every thread)
   if (tid < 2) {
     Shared& x = shared[tid];
@@ -498,7 +500,8 @@ __device__ __forceinline__ void join_shared(const AttnX8Params& p, Shared* share
           o.z = fmaf(y.z, k, o.z);
           o.w = fmaf(y.w, k, o.w);
         }
-        store_row<D>(p, x.q0, x.head, x.row0 + (u0 + u) / (D / 4), (u0 + u) % (D / 4), o, high, all, log2_scale);
+        store_row<D>(p, x.q0, x.head, x.row0 + (u0 + u) / (D / 4), (u0 + u) % (D / 4), o, high, all, log2_scale,
+                     ratio);
       }
       __syncthreads();
     }
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
         }
 
         // ---- softmax of the page
-        const float kscale = e8m0_value(page_codes & 0xFF), vscale = e8m0_value(page_codes >> 8);
+        const float kscale = e8m0_value(page_codes & 0xFF), vscale = e8m0_value(page_codes >> 8) * kUnP;
         uint32_t pf[NT][4][2];
         float alpha[NT][2];
 #pragma unroll
@@ -949,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
           den += top == -INFINITY ? 0.0f : t_ml.y * ex2(t_ml.x - top);
         }
         if (whole) {
-          store_row<D>(p, s.q0, head, r, d4, sum, top, den, kLog2P);
+          store_row<D>(p, s.q0, head, r, d4, sum, top, den, kLog2P, 1.0f / kUnP);
         } else {
           const int lr = (w * NT + nt) * 8 + row;
           *reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + d4 * 4) = sum;
@@ -961,7 +964,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, RW>::kThreads, 1)
     }
   }
 
-  join_shared<D, C::kRows, C::kWarps>(p, shared, smem, tid, kLog2P);
+  join_shared<D, C::kRows, C::kWarps>(p, shared, smem, tid, kLog2P, 1.0f / kUnP);
 
   // Every copy issued has been waited for, as each page of the run is
   // consumed. After a wait that gave up, the copies in flight get their time

@@ -480,6 +480,20 @@ def test_attention_loud_pages_behind_the_mask(loud, group, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,group", [(1, 5), (2, 8), (9, 8)])
+@pytest.mark.parametrize("kv", [300, 9001])  # one CTA's pages; parts of many
+@pytest.mark.parametrize("amp", [2.0 ** 119, 2.0 ** 100, 2.0 ** -100, 2.0 ** -116])
+def test_attention_values_near_the_ends_of_the_range(amp, kv, n, group, d):
+    """Values up to bf16's largest and down to its smallest normal ones; what is
+    below that is rounded to bf16's multiples of 2^-133."""
+    c = Cache([kv], 1, d, seed=n)
+    k = c.rng.standard_normal((kv, 1, d)) / 2
+    v = amp * np.clip(c.rng.standard_normal((kv, 1, d)), -5, 5)
+    c.blocks, c.codes = A.append(c.blocks, c.codes, A.bf16_rne(k), A.bf16_rne(v), c.table, [0], [0, kv])
+    _check_attn(c, [n], group, tiny=2.0 ** -133)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("n,group", [(3, 16), (17, 8)])
 def test_attention_many_rows_of_one_long_sequence(d, n, group):
     c = Cache([9001], 1, d, seed=n).fill()
