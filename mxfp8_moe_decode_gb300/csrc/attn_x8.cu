@@ -57,6 +57,15 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
       (lse && !aligned(lse, 4)) || (status && !aligned(status, 4)))
     return MOE_ERR_ALIGN;
   if (ldq < static_cast<int64_t>(q_heads) * cache->head_dim) return MOE_ERR_ARG;
+  const int max_q = seqs->cu_q ? (seqs->max_q < seqs->tokens ? seqs->max_q : seqs->tokens) : 1;
+  const int rows = max_q > (1 << 20) / group ? 1 << 20 : max_q * group;
+  // Rows, the list of pages and its cut into equal runs (rounded up: at most a
+  // position a CTA more) are counted in 32 bits, whatever the lengths on the device.
+  if (static_cast<long long>(seqs->tokens) * group * group > UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const long long groups =
+      static_cast<long long>(seqs->tokens) * group / attn_x8_group_rows(cache->head_dim, rows) + seqs->seqs;
+  if (groups * cache->kv_heads > (INT32_MAX - kMaxGrid) / (static_cast<long long>(seqs->max_pages) + kItemCost))
+    return MOE_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -64,14 +73,6 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
     return MOE_ERR_CUDA;
   }
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  const int max_q = seqs->cu_q ? (seqs->max_q < seqs->tokens ? seqs->max_q : seqs->tokens) : 1;
-  const int rows = max_q > (1 << 20) / group ? 1 << 20 : max_q * group;
-  // rows and the list of pages are counted in 32 bits, whatever the lengths on the device
-  if (static_cast<long long>(seqs->tokens) * group * group > UINT32_MAX) return MOE_ERR_UNSUPPORTED;
-  const long long groups =
-      static_cast<long long>(seqs->tokens) * group / attn_x8_group_rows(cache->head_dim, rows) + seqs->seqs;
-  if (groups * cache->kv_heads > INT32_MAX / (seqs->max_pages + 8ll))
-    return MOE_ERR_UNSUPPORTED;
   if (workspace_size < workspace_bytes(grid, cache->head_dim, rows)) return MOE_ERR_ARG;
   AttnX8Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);

@@ -72,7 +72,6 @@ namespace attn {
 
 constexpr float kLog2P = 14.0f;  // P and its sum are held times 2^14
 constexpr float kUnP = 0x1p-14f;  // O is not: it has fp32's whole range for values as large as bf16's
-constexpr int kItemCost = 10;    // starting and joining an item costs about as much as its pages
 
 template <int D, int NT, int RW>
 struct Cfg {
@@ -226,7 +225,8 @@ __device__ __forceinline__ Seq load_seq(const AttnX8Params& p, int b) {
   return s;
 }
 
-// List positions of one item: kItemCost for its start and end, then its pages.
+// List positions of one item: kItemCost for its start and end (they cost about
+// as much as that many pages), then its pages.
 __device__ __forceinline__ int item_size(const Seq& s) { return s.pages + kItemCost; }
 
 // A walk over a run [w, end) of the work list, segment by segment: the run's
@@ -356,7 +356,7 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
     walk.end = walk.w + min(len, walk.s.pages - first);
   } else {
     walk.w = at;
-    walk.end = min(at + per, total);
+    walk.end = at + min(per, total - at);
   }
   return true;
 }

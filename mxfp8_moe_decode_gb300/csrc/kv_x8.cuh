@@ -26,6 +26,7 @@
 namespace moe {
 
 constexpr int kPageTokens = MOE_KV_PAGE_TOKENS;
+constexpr int kItemCost = 10;  // pages that an item of the attention's work list counts for beside its own
 static_assert(kPageTokens == 64, "the images' chunk permutations are written for 64 tokens");
 
 // error bits in the status word of the cache kernels

@@ -124,6 +124,22 @@ def test_attention_refusals(L):
     assert call(ldq=1016) == MOE_ERR_ARG
 
 
+@pytest.mark.parametrize("kv_heads,group,max_pages,seqs,max_q,refused", [
+    # one row a sequence: an item of 1 page takes 1 + 10 positions, (2^20 / 8 + 2^20) * kv_heads items at most
+    (200, 1, 1, 1 << 20, 1, True), (166, 1, 1, 1 << 20, 1, True), (165, 1, 1, 1 << 20, 1, False),
+    (108, 1, 7, 1 << 20, 1, True), (107, 1, 7, 1 << 20, 1, False),
+    (16, 1, 100, 1 << 20, 1, False), (17, 1, 100, 1 << 20, 1, True),
+    (1, 256, 1, 1 << 16, 1, True), (1, 256, 1, (1 << 16) - 1, 1, False),  # tokens * group^2 beside it
+])
+def test_attention_work_list_fits_32_bits(L, kv_heads, group, max_pages, seqs, max_q, refused):
+    c = _cache(kv_heads=kv_heads, head_dim=64)
+    s = _seqs(cu_q=None, seqs=seqs, tokens=seqs, max_pages=max_pages, max_q=max_q)
+    heads = kv_heads * group
+    # (a workspace of no bytes: what is not refused here is refused for that, or for want of a GPU)
+    rc = L.moe_attn_x8(c, s, P[5], heads * 64, heads, 0.1, 0, 0, P[6], None, P[7], 0, None, None)
+    assert (rc == MOE_ERR_UNSUPPORTED) == refused, rc
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
