@@ -14,7 +14,7 @@
 // no two CTAs write the same bytes, nothing is atomic. The pages are found
 // without a scan: sequence b gets the slots cu_q[b] / 64 + 2 b .. , which are
 // at least as many as the pages its tokens can touch, and a CTA whose slot has
-// none leaves. Keys are rows; values go through shared memory (16 tokens x 4
+// none leaves (all do where the rows' starts do not ascend). Keys are rows; values go through shared memory (16 tokens x 4
 // dims per thread, transposed with byte permutes) so that whole 16-byte
 // chunks are stored.
 // 8 heads of 128: two prompts of 4100 tokens 10.7 us (50 MB, 4.7 TB/s: 2100 CTAs
@@ -111,13 +111,19 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   } else {
     const long long slot = blockIdx.x;
     int below = 0;
+    bool falls = false;
     for (int i0 = 0; i0 < p.seqs; i0 += kThreads) {
       const int i = i0 + tid;
       if (i < p.seqs) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.start + i));  // read next
+      const int c = i < p.seqs ? p.cu_q[i] : 0;
+      falls |= i < p.seqs && c > p.cu_q[i + 1];
       const bool le = i < p.seqs &&
-                      static_cast<long long>(min(max(p.cu_q[i], 0), p.tokens) / kPageTokens) +
-                              2ll * i <= slot;
+                      static_cast<long long>(min(max(c, 0), p.tokens) / kPageTokens) + 2ll * i <= slot;
       below += __syncthreads_count(le);
+    }
+    if (__syncthreads_or(falls)) {  // starts that do not ascend
+      if (tid == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, kKvErrLength);
+      return;
     }
     b = max(below - 1, 0);
     c0 = min(max(p.cu_q[b], 0), p.tokens);

@@ -234,6 +234,23 @@ def test_append_reports_bad_pages_and_lengths():
         assert np.array_equal(blocks.cpu().numpy(), c.blocks) and np.array_equal(codes.cpu().numpy(), c.codes)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cu_q", [[0, 6, 2, 8], [0, 3, 1, 2], [0, 8, 0, 8], [5, 0, 8, 8]])
+def test_append_refuses_row_starts_that_do_not_ascend(cu_q, d):
+    c = Cache([20, 64, 100], 2, d, seed=2, spare=5, extra_width=1).fill()
+    c.table[:] = np.arange(9).reshape(3, 3)  # (no page twice)
+    blocks, codes, table = c.gpu()
+    x = torch.ones(8, 2, d, dtype=torch.bfloat16, device=DEV)
+    status = i32([0])
+    M.kv_append_x8(blocks, codes, x, x, table, i32([20, 64, 100]), cu_q=i32(cu_q), status=status)
+    torch.cuda.synchronize()
+    assert status.item() == _lib.KV_STATUS_LENGTH
+    assert np.array_equal(blocks.cpu().numpy(), c.blocks) and np.array_equal(codes.cpu().numpy(), c.codes)
+    M.kv_append_x8(blocks, codes, x, x, table, i32([20, 64, 100]), cu_q=i32(cu_q))  # (without a status)
+    torch.cuda.synchronize()
+    assert np.array_equal(blocks.cpu().numpy(), c.blocks) and np.array_equal(codes.cpu().numpy(), c.codes)
+
+
 # ---------------------------------------------------------------- the attention
 def _check_attn(c, n, heads, window=0, sinks=0, cu=True, q=None, max_q=None, lens=None, scale=None, ws=None, tiny=0.0):
     lens = c.lens if lens is None else lens
