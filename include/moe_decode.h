@@ -449,8 +449,7 @@ typedef struct moe_kv_seqs {
 #define MOE_KV_STATUS_TIMEOUT 1 /* a bounded wait expired: outputs unspecified, clear the workspace */
 #define MOE_KV_STATUS_PAGE 2    /* a page id outside [0, pages): its tokens are left out */
 #define MOE_KV_STATUS_LENGTH 4  /* a length below 0 or beyond the page table: clamped / not written;
-                                   append: cu_q falls anywhere: nothing written;
-                                   attention: cu_q gives more rows than `tokens`: nothing written */
+                                   cu_q falls anywhere: nothing written */
 
 /*
  * Appends new keys and values: row r of k and v (bf16, kv_heads x head_dim

@@ -275,8 +275,8 @@ template <int kRows, int kUneven>
 __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int lane, int warp, Walk& walk,
                                          int& per, int& parts) {
   parts = 0;
-  int total = 0, items = 0, longest = 0, tokens = 0;
-  bool odd_len = false;
+  int total = 0, items = 0, longest = 0;
+  bool odd_len = false, falls = false;
   Seq head = {};  // of sequence `lane`, which the search below begins with
   for (int b = lane; b < p.seqs; b += 32) {
     const Seq s = load_seq<kRows>(p, b);
@@ -286,10 +286,11 @@ __device__ __forceinline__ bool find_run(const AttnX8Params& p, int teams, int l
     total += item_size(s) * n;
     items += n;
     longest = max(longest, s.pages);
-    tokens = min(tokens + s.n, 1 << 25);  // (32 lanes' fit 32 bits)
+    falls |= p.cu_q != nullptr && __ldg(p.cu_q + b) > __ldg(p.cu_q + b + 1);
   }
-  // Starts that do not ascend: the list could be longer than 32 bits count.
-  const bool disorder = static_cast<int>(__reduce_add_sync(0xffffffffu, tokens)) > p.tokens;
+  // Starts that do not ascend: rows of two sequences could be the same, and the
+  // list longer than 32 bits count.
+  const bool disorder = __any_sync(0xffffffffu, falls);
   odd_len |= disorder;
   if (odd_len && blockIdx.x == 0 && warp == 0 && p.status) atomicOr(p.status, kKvErrLength);
   total = __reduce_add_sync(0xffffffffu, total);

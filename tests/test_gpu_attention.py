@@ -673,6 +673,29 @@ def test_attention_refuses_row_starts_that_do_not_ascend(d, max_q):
     assert status.item() == 0 and torch.isfinite(out).all() and not (out == 5).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("max_q", [1, 2, 8, 40])  # 2, 4, 16 and 80 rows: each kernel
+@pytest.mark.parametrize("cu_q", [[0, 30, 10, 40], [0, 20, 19, 21], [0, 40, 0, 40], [5, 0, 40, 40]])
+def test_attention_refuses_any_fall_of_the_row_starts(cu_q, max_q, d):
+    """Also where the sequences' rows together are no more than the call's, and in
+    every kernel (by max_q of 40 rows)."""
+    c = Cache([100, 100, 100], 1, d, seed=2).fill()
+    q = torch.ones(40, 2, d, dtype=torch.bfloat16, device=DEV)
+    blocks, codes, table = c.gpu()
+    ws = M.attn_x8_workspace(DEV)
+    out = torch.full_like(q, 5.0)
+    status = i32([0])
+    args = dict(max_q=max_q, out=out, workspace=ws, status=status)
+    M.attn_x8(q, blocks, codes, table, i32(c.lens), cu_q=i32(cu_q), **args)
+    torch.cuda.synchronize()
+    assert status.item() == _lib.KV_STATUS_LENGTH and (out == 5).all()
+    status.zero_()
+    M.attn_x8(q, blocks, codes, table, i32(c.lens), cu_q=i32([0, 30, 30, 40]), **args)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and torch.isfinite(out).all() and not (out == 5).all()
+    assert not ws[:4096].any()
+
+
 def test_bindings_refuse_wrong_tensors():
     """Wrong types, shapes, devices and strides, one argument at a time."""
     d = 64
