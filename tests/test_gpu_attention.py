@@ -348,6 +348,27 @@ def test_attention_variants_agree():
         _check_attn(c, [1, 1], 6, q=q, max_q=max_q)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 5)])
+def test_attention_kernels_agree(window, sinks, d):
+    """The same rows in every kernel: a sequence of 40 rows leaves max_q of 1, 2, 4
+    and 40 (6, 12, 24 and 240 rows per key/value head) as they are given. Their
+    weights are rounded in other places: within both bounds of one another."""
+    c = Cache([700, 90, 300], 2, d, seed=9).fill()
+    n = [1, 40, 2]
+    q = torch.from_numpy(c.rng.standard_normal((43, 12, d))).bfloat16().to(DEV)
+    outs = [_check_attn(c, n, 12, window, sinks, q=q, max_q=max_q) for max_q in (1, 2, 4, 40)]
+    want, _, spread, slack = A.attention(f64(q), A.cache_values(c.blocks, c.codes), c.table, c.lens, [0, 1, 41, 43],
+                                         d ** -0.5, window, sinks)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * slack[..., None]) * spread
+    seen = [f64(o) for o, _ in outs]
+    for i in range(4):
+        for j in range(i):
+            assert (np.abs(seen[i] - seen[j]) <= 2 * bound).all()
+    # (not one kernel four times: some roundings differ)
+    assert any(not np.array_equal(seen[i], seen[0]) for i in range(1, 4))
+
+
 @pytest.mark.parametrize("amp,qamp", [(40.0, 1.0), (1.0, 2.0 ** 60), (2.0 ** -60, 1.0), (1.0, 0.0)])
 def test_attention_peaked_flat_and_far_scales(amp, qamp):
     """Scores of hundreds, rows of large, tiny and zero values."""
