@@ -498,8 +498,8 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
  *    exact down to 2^-28 of the row's largest value
  *  more rows: weights of 11 bits down to 2^-21 of the row's largest (2^(k - 21)
  *    on a page whose values' scale is 2^-k, k up to 8, of an earlier page's),
- *    0 below 2^-32; q off by at most 2^-18 of the row's largest value; pages
- *    2^80 and more quieter than what the row has summed so far may lose bits
+ *    0 below 2^-32; q off by at most 2^-18 of the row's largest value; beside
+ *    pages that weigh and are 2^80 or more louder the quieter may lose bits
  *
  * workspace: device memory (16-byte aligned) of at least
  * MOE_ATTN_X8_WORKSPACE_BYTES (enough for every call), zero before its first
