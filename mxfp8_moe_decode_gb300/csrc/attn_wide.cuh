@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
           const int vc = codes >> 8;
           const bool rise = ref != -INFINITY && top > ref + kHeadroom;
-          const bool counts = top != -INFINITY && (rise || ref == -INFINITY || top >= ref - kNothing);
+          const bool counts = top > fmaxf(ref - kNothing, -FLT_MAX);
           const bool turn = counts && vref >= 0 && (vc > vref || vc < vref - kQuieter);
           if (counts && vref < 0) vref = vc;
           if (__any_sync(0xffffffffu, rise || turn)) {
@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
       const size_t at_out = static_cast<size_t>(s.q0 + token) * (p.kv_heads * p.group) +
                             walk.head * p.group + r - token * p.group;
       // (behind the value scale: the two together may leave fp32's exponents)
-      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : __frcp_rn(l) * (1.0f / kUnPWide);
+      const float inv = l == 0.0f ? 0.0f : __frcp_rn(l) * (1.0f / kUnPWide);
 #pragma unroll 2
       for (int d = 0; d < D; d += 16) {
         float x[16], y[16];
@@ -876,13 +876,12 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1) attn_wide_kernel(cons
         for (int k = 0; k < 16; ++k) {
           x[k] *= wa;
           if (both) x[k] = fmaf(y[k], wb, x[k]);
-          x[k] *= inv;
         }
         if (r < rows) {
           if (whole) {
             __align__(16) __nv_bfloat162 z[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            for (int k = 0; k < 8; ++k) z[k] = __floats2bfloat162_rn(x[2 * k] * inv, x[2 * k + 1] * inv);
             uint4* dst = reinterpret_cast<uint4*>(p.out + at_out * D + d);
             dst[0] = reinterpret_cast<const uint4*>(z)[0];
             dst[1] = reinterpret_cast<const uint4*>(z)[1];
