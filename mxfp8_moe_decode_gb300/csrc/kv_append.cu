@@ -17,7 +17,7 @@
 // none leaves (all do where the rows' starts do not ascend). Keys are rows; values go through shared memory (16 tokens x 4
 // dims per thread, transposed with byte permutes) so that whole 16-byte
 // chunks are stored.
-// 8 heads of 128: two prompts of 4100 tokens 10.7 us (50 MB, 4.7 TB/s: 2100 CTAs
+// 8 heads of 128: two prompts of 4100 tokens 10.8 us (50 MB, 4.7 TB/s: 2100 CTAs
 // are 1.7 times what the SMs hold, and each is a chain of page lookup, loads,
 // maximum and stores; more resident CTAs by fewer registers took 15 to 18 us);
 // 48 sequences of one token 3.5 us, one such chain. The values' CTAs, which do
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     const long long slot = blockIdx.x;
     int below = 0;
     bool falls = false;
+#pragma unroll 1  // (unrolled, the code of one token a sequence grew too: 3.8 us)
     for (int i0 = 0; i0 < p.seqs; i0 += kThreads) {
       const int i = i0 + tid;
       if (i < p.seqs) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.start + i));  // read next
