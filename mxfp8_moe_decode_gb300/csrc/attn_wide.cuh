@@ -35,7 +35,7 @@
 // 770 cycles, the softmax about 1000 beside it. mma.sync on the same work takes
 // 142 cycles for every 8 rows and converts K and V once per 16 rows: 238 us
 // where this takes 54 (48 query tokens over 32k, 8 heads with 5 query heads
-// each), 66 where it takes 37 (6 sequences of 8 tokens over 3k to 8k). Of the
+// each), 66 where it takes 36 (6 sequences of 8 tokens over 3k to 8k). Of the
 // 54 us about 28 are the pages (27 a CTA, 2050 cycles each), 3.5 the start, 5
 // more pass to the first scores, 4 are the output, the rest the join of 19 parts.
 //

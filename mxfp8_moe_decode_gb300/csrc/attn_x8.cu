@@ -13,7 +13,7 @@ namespace moe {
 // that share the pages (D = 128; 48 sequences over 3.5k tokens, 8 heads: 77 us,
 // two tiles on one warp 94) or two tiles on one warp (D = 64: 49 us, two warps
 // 52 to 58). Beyond: the tcgen05 kernel's two tiles of 128 (32 rows over 12 such
-// sequences: 44 us, two tiles on each of two warps 55; for 16 rows it takes
+// sequences: 43 us, two tiles on each of two warps 55; for 16 rows it takes
 // 132). Heads of 256, whose key rows are not an operand tile of it, have pages
 // shared by two or three warps: a group of 16 rows takes 51 us where one of 24
 // takes 64 (12 sequences), so the split of less work in that ratio is chosen.

@@ -14,13 +14,13 @@
 // no two CTAs write the same bytes, nothing is atomic. The pages are found
 // without a scan: sequence b gets the slots cu_q[b] / 64 + 2 b .. , which are
 // at least as many as the pages its tokens can touch, and a CTA whose slot has
-// none leaves (all do where the rows' starts do not ascend). Keys are rows; values go through shared memory (16 tokens x 4
-// dims per thread, transposed with byte permutes) so that whole 16-byte
-// chunks are stored.
+// none leaves (all do where the rows' starts do not ascend). Keys are rows;
+// values go through shared memory (16 tokens x 4 dims per thread, transposed
+// with byte permutes) so that whole 16-byte chunks are stored.
 // 8 heads of 128: two prompts of 4100 tokens 10.8 us (50 MB, 4.7 TB/s: 2100 CTAs
 // are 1.7 times what the SMs hold, and each is a chain of page lookup, loads,
 // maximum and stores; more resident CTAs by fewer registers took 15 to 18 us);
-// 48 sequences of one token 3.5 us, one such chain. The values' CTAs, which do
+// 48 sequences of one token 3.6 us, one such chain. The values' CTAs, which do
 // more, come first in the grid (the keys' first: 11.4 us).
 #include "internal.cuh"
 #include "kv_x8.cuh"
