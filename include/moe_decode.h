@@ -507,11 +507,12 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
  * GPU need workspaces of their own. One or two kernels on `stream`; no
  * allocation, no synchronisation, capture safe. Only pages that some row sees are read.
  * Errors as moe_kv_append_x8, and MOE_ERR_ARG for a scale that is not positive
- * and finite, a negative window or sinks, max_q < 1, q_heads not a multiple of
- * kv_heads, or a workspace that is too small; MOE_ERR_UNSUPPORTED for more
- * than 256 query heads per key/value head, or where tokens * (q_heads /
- * kv_heads)^2 passes 2^32 or kv_heads * (max_pages + 10) * (seqs + tokens *
- * q_heads / kv_heads / 8) passes 2^31 - 385 (many rows: / 16, 24 or 256 in place of / 8).
+ * and, times log2 e, finite, a negative window or sinks, max_q < 1, q_heads not
+ * a multiple of kv_heads, or a workspace that is too small; MOE_ERR_UNSUPPORTED
+ * for more than 256 query heads per key/value head, or where tokens * (q_heads /
+ * kv_heads)^2 passes 2^32 - 1 or kv_heads * (max_pages + 10) * (seqs + tokens *
+ * q_heads / kv_heads / 8) passes 2^31 - 385 (more rows: / 16, 24 or 256 in place
+ * of / 8).
  */
 #define MOE_ATTN_X8_WORKSPACE_BYTES (48u << 20)
 int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* q, int64_t ldq,

@@ -49,7 +49,8 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   if (q_heads < 1 || q_heads % cache->kv_heads) return MOE_ERR_ARG;
   const int group = q_heads / cache->kv_heads;
   if (group > 256) return MOE_ERR_UNSUPPORTED;
-  if (!(scale > 0.0f) || std::isinf(scale) || window < 0 || sinks < 0) return MOE_ERR_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || std::isinf(scale_log2) || window < 0 || sinks < 0) return MOE_ERR_ARG;
   if (seqs->max_q < 1) return MOE_ERR_ARG;
   if (seqs->tokens == 0) return MOE_OK;
   if (!q || !out || !workspace) return MOE_ERR_ARG;
@@ -100,7 +101,7 @@ extern "C" int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, c
   // keeps position - window in 32 bits for rows before the first token too.
   p.window = window < p.max_kv ? window : 0;
   p.sinks = sinks;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (cache->head_dim) {

@@ -140,6 +140,16 @@ def test_attention_work_list_fits_32_bits(L, kv_heads, group, max_pages, seqs, m
     assert (rc == MOE_ERR_UNSUPPORTED) == refused, rc
 
 
+def test_attention_scale_is_finite_in_log2_units(L):
+    """Scores are computed times log2 e: a scale that is infinite there is refused
+    (it made NaN of scores of 0). No rows: nothing else is looked at."""
+    def call(scale):
+        return L.moe_attn_x8(_cache(), _seqs(tokens=0), None, 1024, 8, scale, 0, 0, None, None, None, 0, None, None)
+
+    assert call(3e38) == MOE_ERR_ARG and call(2.4e38) == MOE_ERR_ARG
+    assert call(2.3e38) == MOE_OK
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
