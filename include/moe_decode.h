@@ -394,6 +394,25 @@ int moe_add_norm_x8(const void* x, int64_t ldx, const void* residual, int64_t ld
                     uint8_t* x8_codes, void* normed, void* stream);
 
 /*
+ * The norms around a block, with its gate and the residual's scale, of M bf16
+ * token rows (device): x is what the block gave,
+ *   b       = x * (mean(x^2) + eps)^(-1/2) * post_w      (post_w null: b = x)
+ *   res_out = bf16(res_scale * residual + block_scale * (gate * b))  (gate null: 1)
+ *   ys      = res_out * (mean(res_out^2) + eps)^(-1/2) * norm_w      (fp32)
+ *   x8, x8_codes, normed = as moe_add_norm_x8's, of ys
+ * computed in fp32 with the one rounding of res_out, which the second norm
+ * reads; x8 and x8_codes are moe_attn_seam_x8's of res_out, bit for bit. gate:
+ * bf16 rows of `hidden` values ldg elements apart, one for each token, or with
+ * ldg = 0 one row for all. post_w and norm_w [hidden]. The rest as
+ * moe_add_norm_x8: strides, in place, limits, capture, errors; MOE_ERR_ARG also
+ * for a scale that is not finite and for 0 < ldg < hidden.
+ */
+int moe_norm_add_norm_x8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                         const void* gate, int64_t ldg, const void* post_w, const void* norm_w,
+                         int M, int hidden, float res_scale, float block_scale, float eps,
+                         void* res_out, uint8_t* x8, uint8_t* x8_codes, void* normed, void* stream);
+
+/*
  * The 8-bit paged key/value cache. A page holds MOE_KV_PAGE_TOKENS tokens;
  * per page, key/value head and kind (0 keys, 1 values) it keeps 64 * head_dim
  * E4M3 bytes and one E8M0 code: byte b under code c stands for
@@ -476,6 +495,57 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
                      int64_t ldk, const void* v, int64_t ldv, int32_t* status, void* stream);
 
 /*
+ * Rotary positions: which dims of a head turn, and how.
+ *  freqs        uint64 [rot / 2] (device, 16-byte aligned): pair i turns by
+ *               freqs[i] * 2^-64 turns per position (a frequency of f radians
+ *               is f / (2 pi) * 2^64; what a long context scales is scaled here)
+ *  first, rot   the dims first .. first + rot - 1 turn, the others are copied;
+ *               first a multiple of 8, rot a multiple of 16, first + rot <= head_dim
+ *  interleaved  0: pair i is (i, i + rot / 2) of them; else (2 i, 2 i + 1)
+ *  scale        factor of cos and sin (finite; the dims that do not turn have none)
+ * A pair (u, v) at position pos becomes bf16(scale * (u cos a - v sin a)) and
+ * bf16(scale * (v cos a + u sin a)) with a = pos * freqs[i] modulo whole turns:
+ * exact up to 2^-33 turns at any 32-bit position; the rest is fp32.
+ */
+typedef struct moe_rope_spec {
+  const uint64_t* freqs;
+  int first;
+  int rot;
+  int interleaved;
+  float scale;
+} moe_rope_spec;
+
+/*
+ * Turns token rows of `heads` heads: x bf16, rows ldx elements apart, into out,
+ * rows ldo elements apart (multiples of 8, at least heads * head_dim), by
+ * positions int32 [tokens] (device; any value). out may be x where the strides
+ * are equal; other overlaps are not allowed. One kernel on `stream`; no
+ * allocation, no synchronisation, capture safe. head_dim a multiple of 16 in
+ * [16, 1024], heads 1..4096. Errors: MOE_ERR_RANGE (tokens < 0 or > 2^24),
+ * MOE_ERR_UNSUPPORTED (dims, or more work than a grid holds: tokens * heads *
+ * head_dim past 2^42), MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_CUDA. A value that is
+ * not finite touches its own pair alone.
+ */
+int moe_rope(const moe_rope_spec* spec, const void* x, int64_t ldx, int tokens, int heads,
+             int head_dim, const int32_t* positions, void* out, int64_t ldo, void* stream);
+
+/*
+ * Rotary positions and the cache's append in one kernel: q (q_heads heads) and k
+ * (the cache's) are turned as moe_rope turns them, q into q_out, k into the
+ * cache with v as moe_kv_append_x8 writes them: bit for bit what the two give
+ * one after the other. positions int32 [tokens] (device), or null: a token's
+ * place in the cache (lens[b] + i). q_out may be q where the strides are equal.
+ * Rows of no sequence, and those of a sequence whose length is refused
+ * (MOE_KV_STATUS_LENGTH), are left as they were in q_out too; a page id out of
+ * range leaves out keys and values only. Strides, limits and errors as
+ * moe_kv_append_x8's and moe_rope's; max_q is not read.
+ */
+int moe_rope_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs,
+                          const moe_rope_spec* spec, const int32_t* positions, const void* q,
+                          int64_t ldq, int q_heads, void* q_out, int64_t ldqo, const void* k,
+                          int64_t ldk, const void* v, int64_t ldv, int32_t* status, void* stream);
+
+/*
  * Attention of query rows over the cache. Row i of the n rows of a sequence
  * with kv = lens[b] tokens sits at position pos = kv - n + i and sees the
  * tokens j <= pos with window == 0, j > pos - window or j < sinks (a sliding
@@ -518,6 +588,30 @@ int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const v
 int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* q, int64_t ldq,
                 int q_heads, float scale, int window, int sinks, void* out, float* lse,
                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Products with 4-bit weights: out[m, n] = bf16(sum_k x[m, k] * w[n, k]).
+ *  w        e2m1x2 u8 [N, K/2] (device, contiguous, 32-byte aligned): column 2j
+ *           in the low nibble of byte j of a row, as the routed experts' rows of
+ *           MOE_ROUTED_E2M1; w_codes u8 [N, K/32] (4-byte aligned): its E8M0 codes,
+ *           one per row per 32 columns (255 stands for NaN)
+ *  x        x_codes null: bf16 [M, K], rows ldx elements apart (a multiple of 8);
+ *           else E4M3 bytes [M, K], rows ldx bytes apart (a multiple of 16), with
+ *           x_codes u8 [M, K/32] (contiguous, 4-byte aligned): MXFP8 rows as
+ *           moe_add_norm_x8 writes them. 16-byte aligned
+ *  out      bf16 [M, N], rows ldo elements apart (any ldo >= N)
+ *  status   int32 (device, 4-byte aligned) or null: MOE_LINEAR_STATUS_TIMEOUT is set
+ *           where a bounded wait expired (out is unspecified then)
+ * The weights are read as they are: nothing is laid out before, nothing is kept.
+ * Products are exact and sums fp32.
+ */
+#define MOE_LINEAR_BF16 0
+#define MOE_LINEAR_MXFP8 1
+#define MOE_LINEAR_STATUS_TIMEOUT 1
+int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes, int M, const uint8_t* w,
+                  const uint8_t* w_codes, int N, int K, void* out, int64_t ldo, void* workspace,
+                  size_t workspace_bytes, int32_t* status, void* stream);
+size_t moe_linear_x4_workspace_bytes(int M, int K, int x_format);
 
 #ifdef __cplusplus
 }

@@ -64,6 +64,15 @@ class KvSeqs(ctypes.Structure):
                 ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int)]
 
 
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("first", ctypes.c_int), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+# products with 4-bit weights
+LINEAR_BF16, LINEAR_MXFP8 = 0, 1
+LINEAR_STATUS_TIMEOUT = 1
+
 _LIB = None
 
 
@@ -109,6 +118,19 @@ def lib() -> ctypes.CDLL:
     i64, fp = ctypes.c_int64, ctypes.c_float
     L.moe_add_norm_x8.argtypes = [vp, i64, vp, i64, vp, ip, ip, fp, vp, vp, vp, vp, vp]
     L.moe_add_norm_x8.restype = ip
+    L.moe_norm_add_norm_x8.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ip, ip, fp, fp, fp, vp, vp, vp,
+                                       vp, vp]
+    L.moe_norm_add_norm_x8.restype = ip
+    L.moe_rope.argtypes = [ctypes.POINTER(RopeSpec), vp, i64, ip, ip, ip, vp, vp, i64, vp]
+    L.moe_rope.restype = ip
+    L.moe_rope_kv_append_x8.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs),
+                                        ctypes.POINTER(RopeSpec), vp, vp, i64, ip, vp, i64, vp, i64, vp,
+                                        i64, vp, vp]
+    L.moe_rope_kv_append_x8.restype = ip
+    L.moe_linear_x4.argtypes = [vp, i64, vp, ip, vp, vp, ip, ip, vp, i64, vp, ctypes.c_size_t, vp, vp]
+    L.moe_linear_x4.restype = ip
+    L.moe_linear_x4_workspace_bytes.argtypes = [ip, ip, ip]
+    L.moe_linear_x4_workspace_bytes.restype = ctypes.c_size_t
     L.moe_kv_append_x8.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), vp, i64, vp,
                                    i64, vp, vp]
     L.moe_kv_append_x8.restype = ip

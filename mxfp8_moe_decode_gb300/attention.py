@@ -1,5 +1,6 @@
 """The attention side of a decode layer, on torch tensors: residual addition +
-RMSNorm + MXFP8, the 8-bit paged key/value cache, and the attention over it.
+RMSNorm + MXFP8 (also with a norm, gate and scales in front), rotary positions,
+the 8-bit paged key/value cache, and the attention over it.
 
 Argument marshalling only, like :mod:`.api`, and in compiled code (csrc/host.cpp):
 tensor shapes, dtypes, devices and strides are checked there (the kernels'
@@ -12,6 +13,7 @@ in device data (page ids, lengths) is reported in the bits of an int32
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -32,7 +34,9 @@ def _host():
             raise ImportError(f"mxfp8_moe_decode_gb300._host: {e} (build it with "
                               "`python -m mxfp8_moe_decode_gb300.build`)") from e
         host.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
-                    for fn in (L.moe_add_norm_x8, L.moe_kv_append_x8, L.moe_attn_x8)))
+                    for fn in (L.moe_add_norm_x8, L.moe_kv_append_x8, L.moe_attn_x8, L.moe_norm_add_norm_x8,
+                               L.moe_rope, L.moe_rope_kv_append_x8, L.moe_linear_x4,
+                               L.moe_linear_x4_workspace_bytes)))
         _bound = host
     return _bound
 
@@ -57,6 +61,70 @@ def add_norm_x8(x: torch.Tensor, residual: torch.Tensor, norm_w: torch.Tensor, e
     """
     return _result((_bound or _host()).add_norm_x8(x, residual, norm_w, eps, res_out, x8, codes, normed),
                    "moe_add_norm_x8")
+
+
+def norm_add_norm_x8(x: torch.Tensor, residual: torch.Tensor, post_w: torch.Tensor | None, norm_w: torch.Tensor,
+                     gate: torch.Tensor | None = None, res_scale: float = 1.0, block_scale: float = 1.0,
+                     eps: float = 1e-6, res_out: torch.Tensor | None = None, x8: torch.Tensor | None = None,
+                     codes: torch.Tensor | None = None, normed: torch.Tensor | None = None):
+    """The norms behind and before a block with its gate (``moe_norm_add_norm_x8``):
+    res_out = bf16(res_scale * residual + block_scale * gate * RMSNorm(x) * post_w),
+    its RMSNorm with ``norm_w``, and the norm's MXFP8, for rows [M, H], M any.
+
+    ``post_w`` None: the block's output x is not normed; ``gate``: bf16 [M, H]
+    (rows may be strided, expanded ones included), [H], or None. The rest, and
+    what is returned, as :func:`add_norm_x8`.
+    """
+    return _result((_bound or _host()).norm_add_norm_x8(x, residual, post_w, norm_w, gate, res_scale, block_scale, eps,
+                                                        res_out, x8, codes, normed), "moe_norm_add_norm_x8")
+
+
+# ---------------------------------------------------------------- rotary positions
+def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: int | None = None,
+               fast: float = 32.0, slow: float = 1.0, inv_freq=None, device="cuda") -> torch.Tensor:
+    """The frequencies of :func:`rope`: int64 [rot / 2], in 2^-64 turns per position
+    (bits of unsigned numbers).
+
+    Pair i turns by base^(-2 i / rot) radians per position, or by ``inv_freq[i]``
+    where that is given. ``factor`` stretches a context: every frequency is
+    divided by it, or with ``trained`` (the length the model was trained on) by
+    parts: pairs that turn ``fast`` times or more within that length keep their
+    frequency, those that turn ``slow`` times or less are divided, the pairs
+    between them are mixed linearly by their number. (The factor of cos and sin
+    that goes with it is :func:`rope`'s ``scale``.)
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and positive, got {rot}")
+    n = rot // 2
+    f = [base ** (-2.0 * i / rot) for i in range(n)] if inv_freq is None else [float(v) for v in inv_freq]
+    if len(f) != n:
+        raise ValueError(f"inv_freq must have {n} values, got {len(f)}")
+    if not factor > 0 or not all(map(math.isfinite, [factor, *f])):
+        raise ValueError("frequencies must be finite, and the factor positive")
+    if trained is None:
+        f = [v / factor for v in f]
+    else:
+        def pair(turns):  # the pair (not whole) that turns so often within the trained length
+            return n * math.log(trained / (turns * 2 * math.pi)) / math.log(base)
+
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+        for i in range(n):
+            keep = 1.0 - min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0)
+            f[i] *= keep + (1.0 - keep) / factor
+    turns = [round(math.ldexp(v / (2 * math.pi), 64)) % (1 << 64) for v in f]
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, first: int = 0, interleaved: bool = False,
+         scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions (``moe_rope``) of x, bf16 [tokens, heads, head_dim], rows may be strided.
+
+    The 2 * len(freqs) dims from ``first`` on turn by positions int32 [tokens]
+    (any values) times freqs (:func:`rope_freqs`); the others are copied. Pairs
+    are (i, i + rot / 2), ``interleaved``: (2 i, 2 i + 1). ``scale`` is a factor of
+    cos and sin. ``out``: rows may be strided; x itself turns in place.
+    """
+    return _result((_bound or _host()).rope(x, positions, freqs, first, interleaved, scale, out), "moe_rope")
 
 
 # ---------------------------------------------------------------- the cache
@@ -96,6 +164,24 @@ def kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, k: torch.Tensor, v: 
     """
     return _result((_bound or _host()).kv_append_x8(blocks, codes, k, v, page_table, start, cu_q, status),
                    "moe_kv_append_x8")
+
+
+def rope_kv_append_x8(blocks: torch.Tensor, codes: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      page_table: torch.Tensor, start: torch.Tensor, freqs: torch.Tensor,
+                      cu_q: torch.Tensor | None = None, positions: torch.Tensor | None = None, first: int = 0,
+                      interleaved: bool = False, scale: float = 1.0, q_out: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None):
+    """:func:`rope` of q and k and :func:`kv_append_x8` of k and v in one kernel
+    (``moe_rope_kv_append_x8``), bit for bit what they give one after the other.
+
+    q: bf16 [tokens, q_heads, head_dim], k and v as :func:`kv_append_x8`'s, all
+    rows may be strided (parts of one projection's output). ``positions`` int32
+    [tokens]; None: a token's place in the cache. Changes blocks and codes in
+    place; returns (q_out, blocks, codes). ``q_out`` may be q itself.
+    """
+    return _result((_bound or _host()).rope_kv_append_x8(blocks, codes, q, k, v, page_table, start, freqs, cu_q,
+                                                         positions, first, interleaved, scale, q_out, status),
+                   "moe_rope_kv_append_x8")
 
 
 def attn_x8_workspace(device="cuda") -> torch.Tensor:

@@ -26,7 +26,8 @@ LIB = os.path.join(HERE, "libmoe_decode.so")
 HOST = os.path.join(HERE, "_host.so")
 HOST_KEY = os.path.join(BUILD, "host.key")  # the torch and the Python that _host.so was built for
 SOURCES = ["api.cu", "seam.cu", "router.cu", "scales.cu", "expert.cu", "combine.cu",
-           "route_static.cu", "attn_seam.cu", "add_norm.cu", "kv_append.cu", "attn_x8.cu",
+           "route_static.cu", "attn_seam.cu", "add_norm.cu", "norm_add_norm.cu", "rope.cu", "kv_append.cu",
+           "linear_x4.cu", "attn_x8.cu",
            "attn_x8_d64.cu", "attn_x8_d128.cu", "attn_x8_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -22,10 +22,19 @@
 // maximum and stores; more resident CTAs by fewer registers took 15 to 18 us);
 // 48 sequences of one token 3.6 us, one such chain. The values' CTAs, which do
 // more, come first in the grid (the keys' first: 11.4 us).
+//
+// With rotary positions (kRope, rope.cuh) the keys' CTAs turn what they loaded
+// and round it to bf16 before anything looks at it, so the cache gets the bytes
+// it would get from keys that another kernel had turned. A chunk's partner (the
+// other halves of its pairs) is a neighbour lane's chunk. Further CTAs of the
+// same grid, behind these, turn the queries: one launch for q, k and v.
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -89,27 +98,145 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t a, uint32_t* red) {
   return a;
 }
 
+struct RopeAppendParams : KvAppendParams {
+  rope::Spec spec;
+  const int* positions;     // [tokens] or null: the tokens' places in the cache
+  const __nv_bfloat16* q;
+  __nv_bfloat16* q_out;
+  long long ldq, ldqo;      // elements between tokens
+  int q_heads, q_groups;    // threads (times D / 16) that share a token's heads
+  unsigned slots, ctas;     // page slots, CTAs of the append (the queries' are behind them)
+};
+
+// The chunks that this thread loaded, turned (v[i]: token tid / kRowChunks + i *
+// kThreads / kRowChunks of the CTA's).
+template <int D, int kMax>
+__device__ __forceinline__ void turn_keys(const RopeAppendParams& p, uint4 (&v)[kMax], int count, int first_row,
+                                          int first_pos) {
+  constexpr int kRowChunks = D / 8;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int chunks = p.spec.rot >> 3, half = chunks >> 1;
+  const int at = tid % kRowChunks - (p.spec.first >> 3);  // among the rotated chunks
+  const bool turns = at >= 0 && at < chunks, low = at < half;
+  // its pairs: 4 of neighbours, or 8 with the chunk `half` further or back
+  const int pair0 = p.spec.interleaved ? 4 * at : 8 * (low ? at : at - half);
+  const int partner = !turns || p.spec.interleaved ? lane : low ? lane + half : lane - half;
+  uint64_t f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = turns && (j < 4 || !p.spec.interleaved) ? __ldg(p.spec.freqs + pair0 + j) : 0;
+#pragma unroll
+  for (int i = 0; i < kMax; ++i) {
+    if ((tid & ~31) + i * kThreads >= count * kRowChunks) break;  // (uniform in the warp)
+    const int row = min((tid + i * kThreads) / kRowChunks, count - 1);
+    const int pos = p.positions ? __ldg(p.positions + first_row + row) : first_pos + row;
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, v[i].x, partner);
+    o.y = __shfl_sync(0xffffffffu, v[i].y, partner);
+    o.z = __shfl_sync(0xffffffffu, v[i].z, partner);
+    o.w = __shfl_sync(0xffffffffu, v[i].w, partner);
+    if (!turns) continue;
+    float c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rope::turn(pos, f[j], p.spec.scale, c[j], s[j]);
+    if (p.spec.interleaved) {
+      rope::turn_neighbours(v[i], c, s);
+    } else {
+#pragma unroll
+      for (int j = 4; j < 8; ++j) rope::turn(pos, f[j], p.spec.scale, c[j], s[j]);
+      uint4 a = low ? v[i] : o, b = low ? o : v[i];
+      rope::turn_halves(a, b, c, s);
+      v[i] = low ? a : b;
+    }
+  }
+}
+
+// The CTA `block` of those that turn the queries. A row's sequence (its place
+// in the cache is its position) is found as the append finds a slot's, from
+// the CTA's first row on by halving.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParams p) {
+__device__ __forceinline__ void turn_queries(const RopeAppendParams& p, unsigned block) {
+  constexpr int kItems = D / 16;
+  const unsigned per = kItems * p.q_groups;
+  const long long u = static_cast<long long>(block) * kThreads + threadIdx.x;
+  const int t0 = static_cast<int>(static_cast<long long>(block) * kThreads / per);
+  const int token = static_cast<int>(u / per);
+  const unsigned rest = static_cast<unsigned>(u - static_cast<long long>(token) * per);
+  int b = token, c0 = token;
+  if (p.cu_q) {
+    int below = 0;
+    bool falls = false;
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.seqs; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      const int c = i < p.seqs ? p.cu_q[i] : 0;
+      falls |= i < p.seqs && c > p.cu_q[i + 1];
+      below += __syncthreads_count(i < p.seqs && c <= t0);
+    }
+    if (__syncthreads_or(falls)) return;  // (the append's CTAs say so)
+    if (token >= p.tokens) return;
+    if (token > t0) {
+      int hi = p.seqs;  // the starts before `below` are <= token, those from hi on are not
+      while (below < hi) {
+        const int mid = (below + hi) >> 1;
+        if (p.cu_q[mid] <= token)
+          below = mid + 1;
+        else
+          hi = mid;
+      }
+    }
+    b = below - 1;
+    if (b < 0 || token >= p.cu_q[b + 1]) return;  // a row of no sequence
+    c0 = max(p.cu_q[b], 0);
+  } else if (token >= p.tokens) {
+    return;
+  }
+  const int start = p.start[b];
+  if (start < 0 || start > (1 << 30)) return;
+  const int pos = p.positions ? __ldg(p.positions + token) : start + (token - c0);
+  rope::Heads h;
+  h.x = reinterpret_cast<const uint4*>(p.q + token * p.ldq);
+  h.out = reinterpret_cast<uint4*>(p.q_out + token * p.ldqo);
+  h.heads = p.q_heads;
+  h.chunks = D / 8;
+  rope::turn_heads(p.spec, h, pos, rest % kItems, rest / kItems, p.q_groups);
+}
+
+template <int D, typename Params>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const Params p) {
+  constexpr bool kRope = !std::is_same<Params, KvAppendParams>::value;
   constexpr int kRowChunks = D / 8;                                // 16-byte chunks of a token
   constexpr int kMax = kPageTokens * kRowChunks / kThreads;        // chunks a thread holds
   constexpr int kPitch = D + 4;                                    // staged token row, bytes
   __shared__ __align__(16) uint8_t stage[kPageTokens * kPitch];
   __shared__ uint32_t red[2][kThreads / 32];
   const int tid = threadIdx.x;
-  const int head = blockIdx.y, kv = 1 - blockIdx.z;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  int slot_index, head, kv;
+  if constexpr (kRope) {  // one row of CTAs in the same order
+    if (blockIdx.x >= p.ctas) {
+      turn_queries<D>(p, blockIdx.x - p.ctas);
+      return;
+    }
+    slot_index = blockIdx.x % p.slots;
+    const int rest = blockIdx.x / p.slots;
+    head = rest % p.kv_heads;
+    kv = 1 - rest / p.kv_heads;
+  } else {
+    slot_index = blockIdx.x;
+    head = blockIdx.y;
+    kv = 1 - blockIdx.z;
+  }
 
   // the slot's sequence and page
   int b, c0, n, page_index;
   if (p.cu_q == nullptr) {
-    b = blockIdx.x;
+    b = slot_index;
     c0 = b;
     n = 1;
     page_index = p.start[b] / kPageTokens;
   } else {
-    const long long slot = blockIdx.x;
+    const long long slot = slot_index;
     int below = 0;
     bool falls = false;
 #pragma unroll 1  // (unrolled, the code of one token a sequence grew too: 3.8 us)
@@ -123,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
       below += __syncthreads_count(le);
     }
     if (__syncthreads_or(falls)) {  // starts that do not ascend
-      if (tid == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, kKvErrLength);
+      if (tid == 0 && slot_index == 0 && p.status) atomicOr(p.status, kKvErrLength);
       return;
     }
     b = max(below - 1, 0);
@@ -154,6 +281,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     v[i] = make_uint4(0, 0, 0, 0);
     if (c < count * kRowChunks)
       v[i] = __ldcs(reinterpret_cast<const uint4*>(src + (c / kRowChunks) * ld) + c % kRowChunks);
+  }
+  if constexpr (kRope) {
+    if (kv == 0) turn_keys<D>(p, v, count, c0 + (t0 - start), t0);
   }
   int page = -1;
   if (page_index < p.max_pages)
@@ -271,19 +401,17 @@ bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q
 }  // namespace
 }  // namespace moe
 
-extern "C" int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* k,
-                                int64_t ldk, const void* v, int64_t ldv, int32_t* status,
-                                void* stream) {
-  using namespace moe;
-  const int rc = kv_check(cache, seqs);
-  if (rc != MOE_OK) return rc;
-  if (seqs->tokens == 0) return MOE_OK;
+namespace moe {
+namespace {
+
+// The checks and parameters that both entry points share; rows > 0 after MOE_OK.
+int append_params(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* k, int64_t ldk, const void* v,
+                  int64_t ldv, int32_t* status, KvAppendParams& p) {
   if (!k || !v) return MOE_ERR_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || ldk % 8 || ldv % 8 || (status && !aligned(status, 4)))
     return MOE_ERR_ALIGN;
   const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
   if (ldk < width || ldv < width) return MOE_ERR_ARG;
-  KvAppendParams p;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
   p.ldk = ldk;
@@ -299,19 +427,78 @@ extern "C" int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* se
   p.max_pages = seqs->max_pages;
   p.pages = cache->pages;
   p.kv_heads = cache->kv_heads;
-  const unsigned slots = p.cu_q ? static_cast<unsigned>(p.tokens / kPageTokens + 2 * p.seqs)
-                                : static_cast<unsigned>(p.seqs);
-  const dim3 grid(slots, cache->kv_heads, 2);
+  return MOE_OK;
+}
+
+unsigned slots_of(const KvAppendParams& p) {
+  return p.cu_q ? static_cast<unsigned>(p.tokens / kPageTokens + 2 * p.seqs) : static_cast<unsigned>(p.seqs);
+}
+
+template <typename Params>
+int launch_append(const Params& p, int head_dim, dim3 grid, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  switch (cache->head_dim) {
-    case 64: e = launch_pdl(kv_append_kernel<64>, grid, dim3(kThreads), 0, st, p); break;
-    case 128: e = launch_pdl(kv_append_kernel<128>, grid, dim3(kThreads), 0, st, p); break;
-    default: e = launch_pdl(kv_append_kernel<256>, grid, dim3(kThreads), 0, st, p); break;
+  switch (head_dim) {
+    case 64: e = launch_pdl(kv_append_kernel<64, Params>, grid, dim3(kThreads), 0, st, p); break;
+    case 128: e = launch_pdl(kv_append_kernel<128, Params>, grid, dim3(kThreads), 0, st, p); break;
+    default: e = launch_pdl(kv_append_kernel<256, Params>, grid, dim3(kThreads), 0, st, p); break;
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* k,
+                                int64_t ldk, const void* v, int64_t ldv, int32_t* status,
+                                void* stream) {
+  using namespace moe;
+  int rc = kv_check(cache, seqs);
+  if (rc != MOE_OK) return rc;
+  if (seqs->tokens == 0) return MOE_OK;
+  KvAppendParams p;
+  rc = append_params(cache, seqs, k, ldk, v, ldv, status, p);
+  if (rc != MOE_OK) return rc;
+  return launch_append(p, cache->head_dim, dim3(slots_of(p), cache->kv_heads, 2), stream);
+}
+
+extern "C" int moe_rope_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs,
+                                     const moe_rope_spec* spec, const int32_t* positions, const void* q,
+                                     int64_t ldq, int q_heads, void* q_out, int64_t ldqo, const void* k,
+                                     int64_t ldk, const void* v, int64_t ldv, int32_t* status,
+                                     void* stream) {
+  using namespace moe;
+  int rc = kv_check(cache, seqs);
+  if (rc != MOE_OK) return rc;
+  if (!spec) return MOE_ERR_ARG;
+  rc = rope::check(spec->freqs, spec->first, spec->rot, cache->head_dim, spec->scale);
+  if (rc != MOE_OK) return rc;
+  if (q_heads < 1 || q_heads > 4096) return MOE_ERR_UNSUPPORTED;
+  if (seqs->tokens == 0) return MOE_OK;
+  RopeAppendParams p;
+  rc = append_params(cache, seqs, k, ldk, v, ldv, status, p);
+  if (rc != MOE_OK) return rc;
+  if (!q || !q_out) return MOE_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 4) || ldq % 8 || ldqo % 8) return MOE_ERR_ALIGN;
+  const int64_t width = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if (ldq < width || ldqo < width || (q == q_out && ldq != ldqo)) return MOE_ERR_ARG;
+  p.spec = {spec->freqs, spec->first, spec->rot, spec->interleaved != 0, spec->scale};
+  p.positions = positions;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.ldq = ldq;
+  p.ldqo = ldqo;
+  p.q_heads = q_heads;
+  p.q_groups = rope::head_groups(p.tokens, q_heads, cache->head_dim);
+  p.slots = slots_of(p);
+  const int64_t ctas = static_cast<int64_t>(p.slots) * cache->kv_heads * 2;
+  const int64_t q_ctas =
+      (static_cast<int64_t>(p.tokens) * p.q_groups * (cache->head_dim / 16) + kThreads - 1) / kThreads;
+  if (ctas + q_ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  p.ctas = static_cast<unsigned>(ctas);
+  return launch_append(p, cache->head_dim, dim3(static_cast<unsigned>(ctas + q_ctas)), stream);
 }

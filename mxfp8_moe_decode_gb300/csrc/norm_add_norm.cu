@@ -1,0 +1,221 @@
+// The norms around a block, with its gate and the residual's scale, of any
+// number of bf16 token rows:
+//   b   = (x * rx) * post_w,  rx = (mean(x^2) + eps)^(-1/2)     (no post_w: b = x)
+//   res = bf16(res_scale * residual + block_scale * (gate * b)) (no gate: 1)
+//   y   = (res * r) * norm_w, r = (mean(res^2) + eps)^(-1/2)
+//   MXFP8 of the fp32 y (E4M3 bytes + one E8M0 code per 32 columns), and
+//   optionally bf16(y).
+// Everything is fp32 up to the one rounding of res, which the next norm reads:
+// it is the row every other reader of the residual stream sees. Both sums of
+// squares have the seam's fixed order (seam.cuh), so y and its bytes equal
+// moe_attn_seam_x8 of res bit for bit, whatever the number of rows.
+//
+// Bound by memory: 4 H bytes in (6 H with a gate per row) and 3.03 H (5.03 H
+// with normed) out per row. One CTA of 128 threads per row, thread i holding
+// the octets i, i + 128, ... of the row as packed bf16 (4 registers an octet)
+// from the loads, all issued before the first use, to the stores: a row is read
+// once, and the two sums cost two exchanges of four floats.
+#include "internal.cuh"
+#include "ptx.cuh"
+#include "seam.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = kSeamOwners;
+
+struct NormAddNormParams {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* residual;
+  const __nv_bfloat16* gate;    // or null
+  const __nv_bfloat16* post_w;  // or null
+  const __nv_bfloat16* norm_w;
+  __nv_bfloat16* res_out;
+  uint8_t* x8;
+  uint8_t* x8c;
+  __nv_bfloat16* normed;        // or null
+  long long ldx, ldr, ldg;      // elements between rows (ldg 0: one gate row for all)
+  int H;
+  float eps, res_scale, block_scale;
+};
+
+// kOct octets a thread (H <= 1024 kOct)
+template <int kOct>
+__global__ void __launch_bounds__(kThreads) norm_add_norm_kernel(const NormAddNormParams p) {
+  const size_t t = blockIdx.x;
+  const int H = p.H;
+  const int noct = H >> 3;
+  const int tid = threadIdx.x;
+  __shared__ float red[2][kThreads / 32];
+  ptx::griddep_wait();  // any input may come from the previous kernel on the stream
+  ptx::griddep_launch_dependents();
+  const uint4* xr = reinterpret_cast<const uint4*>(p.x + t * p.ldx);
+  const uint4* rr = reinterpret_cast<const uint4*>(p.residual + t * p.ldr);
+  const uint4* gr = reinterpret_cast<const uint4*>(p.gate + t * p.ldg);
+  const uint4* pr = reinterpret_cast<const uint4*>(p.post_w);
+  const uint4* wr = reinterpret_cast<const uint4*>(p.norm_w);
+  const bool gated = p.gate != nullptr, post = p.post_w != nullptr;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 s[kOct], b[kOct], g[kOct];
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const int o = tid + i * kThreads;
+    const bool in = o < noct;
+    b[i] = in ? __ldcs(xr + o) : zero;
+    s[i] = in ? __ldcs(rr + o) : zero;
+    g[i] = in && gated ? (p.ldg ? __ldcs(gr + o) : __ldg(gr + o)) : zero;
+  }
+  float rx = 1.0f;
+  if (post) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      if (tid + i * kThreads < noct) {
+        float v[8];
+        unpack_bf16x8(b[i], v);
+        ss = seam_sumsq_octet(v, ss);
+      }
+    }
+    ss = seam_warp_sum(ss);
+    if ((tid & 31) == 0) red[0][tid >> 5] = ss;
+    __syncthreads();
+    rx = seam_scale(red[0], H, p.eps);
+  }
+  float ss = 0.0f;
+  uint4* ro = reinterpret_cast<uint4*>(p.res_out + t * H);
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const int o = tid + i * kThreads;
+    if (o < noct) {
+      float x[8], r[8], m[8];
+      unpack_bf16x8(b[i], x);
+      unpack_bf16x8(s[i], r);
+      if (post) {
+        unpack_bf16x8(__ldg(pr + o), m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (x[j] * rx) * m[j];
+      }
+      if (gated) {
+        unpack_bf16x8(g[i], m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= m[j];
+      }
+      __align__(16) __nv_bfloat162 q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[j] = __floats2bfloat162_rn(fmaf(p.res_scale, r[2 * j], p.block_scale * x[2 * j]),
+                                     fmaf(p.res_scale, r[2 * j + 1], p.block_scale * x[2 * j + 1]));
+      s[i] = *reinterpret_cast<const uint4*>(q);
+      ro[o] = s[i];
+      unpack_bf16x8(s[i], r);
+      ss = seam_sumsq_octet(r, ss);
+    }
+  }
+  ss = seam_warp_sum(ss);
+  if ((tid & 31) == 0) red[1][tid >> 5] = ss;
+  __syncthreads();
+  const float r = seam_scale(red[1], H, p.eps);
+
+#pragma unroll
+  for (int i = 0; i < kOct; ++i) {
+    const int o = tid + i * kThreads;
+    if (i * kThreads >= noct) break;  // uniform across the CTA
+    const bool in = o < noct;
+    float v[8], w[8], y[8];
+    unpack_bf16x8(in ? s[i] : zero, v);
+    unpack_bf16x8(in ? __ldg(wr + o) : zero, w);
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = (v[j] * r) * w[j];
+      amax = fmaxf(amax, fabsf(y[j]));
+    }
+    // the 32-group's amax over its four lanes
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int code = mx_code(amax);
+    const float mul = mx_mul(code);
+    if (in) {
+      uint2 q;
+      q.x = static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[0] * mul), clamp_e4m3(y[1] * mul))) |
+            (static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[2] * mul), clamp_e4m3(y[3] * mul))) << 16);
+      q.y = static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[4] * mul), clamp_e4m3(y[5] * mul))) |
+            (static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[6] * mul), clamp_e4m3(y[7] * mul))) << 16);
+      reinterpret_cast<uint2*>(p.x8 + t * H)[o] = q;
+      if ((o & 3) == 0) p.x8c[t * (H >> 5) + (o >> 2)] = static_cast<uint8_t>(code);
+      if (p.normed) {
+        __align__(16) __nv_bfloat162 n[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+        reinterpret_cast<uint4*>(p.normed + t * H)[o] = *reinterpret_cast<const uint4*>(n);
+      }
+    }
+  }
+}
+
+template <int kOct>
+cudaError_t launch(const NormAddNormParams& p, int M, cudaStream_t s) {
+  return launch_pdl(norm_add_norm_kernel<kOct>, dim3(M), dim3(kThreads), 0, s, p);
+}
+
+bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_norm_add_norm_x8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                    const void* gate, int64_t ldg, const void* post_w,
+                                    const void* norm_w, int M, int hidden, float res_scale,
+                                    float block_scale, float eps, void* res_out, uint8_t* x8,
+                                    uint8_t* x8_codes, void* normed, void* stream) {
+  using namespace moe;
+  if (M < 0) return MOE_ERR_RANGE;
+  if (hidden % 32 || hidden < 32 || hidden > 8 * kSeamOwners * kSeamMaxOct)
+    return MOE_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f)) return MOE_ERR_ARG;
+  // (a difference of itself is 0 for finite numbers only)
+  if (res_scale - res_scale != 0.0f || block_scale - block_scale != 0.0f) return MOE_ERR_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !residual || !norm_w || !res_out || !x8 || !x8_codes) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gate, 16) || !aligned(post_w, 16) ||
+      !aligned(norm_w, 16) || !aligned(res_out, 16) || !aligned(x8, 16) || !aligned(normed, 16))
+    return MOE_ERR_ALIGN;
+  if (ldx < hidden || ldr < hidden || (gate && ldg != 0 && ldg < hidden)) return MOE_ERR_ARG;
+  if (ldx % 8 || ldr % 8 || (gate && ldg % 8)) return MOE_ERR_ALIGN;
+  // in place only where the rows coincide
+  if ((res_out == residual && ldr != hidden) || (res_out == x && ldx != hidden)) return MOE_ERR_ARG;
+  NormAddNormParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.gate = static_cast<const __nv_bfloat16*>(gate);
+  p.post_w = static_cast<const __nv_bfloat16*>(post_w);
+  p.norm_w = static_cast<const __nv_bfloat16*>(norm_w);
+  p.res_out = static_cast<__nv_bfloat16*>(res_out);
+  p.x8 = x8;
+  p.x8c = x8_codes;
+  p.normed = static_cast<__nv_bfloat16*>(normed);
+  p.ldx = ldx;
+  p.ldr = ldr;
+  p.ldg = gate ? ldg : 0;
+  p.H = hidden;
+  p.eps = eps;
+  p.res_scale = res_scale;
+  p.block_scale = block_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch ((hidden / 8 + kThreads - 1) / kThreads) {
+    case 1: e = launch<1>(p, M, st); break;
+    case 2: e = launch<2>(p, M, st); break;
+    case 3: e = launch<3>(p, M, st); break;
+    case 4: e = launch<4>(p, M, st); break;
+    case 5: e = launch<5>(p, M, st); break;
+    case 6: e = launch<6>(p, M, st); break;
+    case 7: e = launch<7>(p, M, st); break;
+    default: e = launch<8>(p, M, st); break;
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}

@@ -1,0 +1,174 @@
+// Rotary positions. Pair i of a head's rotated dims turns by the angle
+//   a = pos * f_i  (in turns),   (u, v) -> scale * (u cos a - v sin a, v cos a + u sin a),
+// with f_i a 64-bit fixed-point number of 2^-64 turns per position. The product
+// with a 32-bit position, modulo 2^64, is the angle without its whole turns,
+// exactly: no position is too far for it (fp32 products of positions and
+// frequencies are off by 0.004 turns at a position of 131072). Of the angle
+// the upper 32 bits are kept (to nearest: off by 2^-33 turns, 7e-10 radians).
+//
+// Sine and cosine: the turn is cut to the nearest quarter, the rest within an
+// eighth of a turn (pi / 4) by their Taylor series: sine up to x^9, cosine up to
+// x^8 (the terms left out are below 2e-9 and 3e-8), in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace moe {
+namespace rope {
+
+constexpr int kPairs = 8;  // pairs that a thread turns together
+
+struct Spec {
+  const uint64_t* freqs;  // [rot / 2]
+  int first, rot;         // the rotated dims first .. first + rot - 1 (multiples of 8 and 16)
+  int interleaved;        // pairs (2 i, 2 i + 1) of them, else (i, i + rot / 2)
+  float scale;
+};
+
+// cos and sin (times scale) of pos * f turns.
+__device__ __forceinline__ void turn(int pos, uint64_t f, float scale, float& c, float& s) {
+  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * f + 0x80000000ull;
+  const uint32_t phase = static_cast<uint32_t>(a >> 32);
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter << 30))) * 0x1.921fb6p-30f;  // 2 pi 2^-32
+  const float z = x * x;
+  float sn = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  sn = fmaf(z, sn, 1.0f / 120.0f);
+  sn = fmaf(z, sn, -1.0f / 6.0f);
+  sn = fmaf(z * x, sn, x);
+  float cs = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
+  cs = fmaf(z, cs, 1.0f / 24.0f);
+  cs = fmaf(z, cs, -0.5f);
+  cs = fmaf(z, cs, 1.0f);
+  sn *= scale;
+  cs *= scale;
+  // a quarter turn: (cos, sin) -> (-sin, cos)
+  const float u = quarter & 1 ? sn : cs, v = quarter & 1 ? cs : sn;
+  c = __uint_as_float(__float_as_uint(u) ^ ((quarter + 1) & 2 ? 0x80000000u : 0u));
+  s = __uint_as_float(__float_as_uint(v) ^ (quarter & 2 ? 0x80000000u : 0u));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The first or the second of each pair (u, v), turned. (One order of operations
+// wherever a pair is turned, so every kernel gives the same bits.)
+__device__ __forceinline__ float first_of(float u, float v, float c, float s) { return fmaf(u, c, -(v * s)); }
+__device__ __forceinline__ float second_of(float u, float v, float c, float s) { return fmaf(v, c, u * s); }
+
+// 8 pairs whose first values are in a, second ones in b.
+__device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const float* c, const float* s) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* y = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float u0 = bf16_lo(x[j]), u1 = bf16_hi(x[j]), v0 = bf16_lo(y[j]), v1 = bf16_hi(y[j]);
+    x[j] = pack(first_of(u0, v0, c[2 * j], s[2 * j]), first_of(u1, v1, c[2 * j + 1], s[2 * j + 1]));
+    y[j] = pack(second_of(u0, v0, c[2 * j], s[2 * j]), second_of(u1, v1, c[2 * j + 1], s[2 * j + 1]));
+  }
+}
+
+// 4 pairs of neighbours.
+__device__ __forceinline__ void turn_neighbours(uint4& a, const float* c, const float* s) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float u = bf16_lo(x[j]), v = bf16_hi(x[j]);
+    x[j] = pack(first_of(u, v, c[j], s[j]), second_of(u, v, c[j], s[j]));
+  }
+}
+
+// A head of 16-byte chunks is cut into dim / 16 items of two chunks: first the
+// rot / 16 that hold 8 pairs each, then the dims that do not turn. Returns
+// whether item j turns (its pairs are 8 j .. 8 j + 7).
+__device__ __forceinline__ bool item_chunks(const Spec& r, int j, int& c0, int& c1) {
+  const int f = r.first >> 3, half = r.rot >> 4;
+  if (j < half) {
+    c0 = f + (r.interleaved ? 2 * j : j);
+    c1 = f + (r.interleaved ? 2 * j + 1 : j + half);
+    return true;
+  }
+  const int u = 2 * (j - half);
+  c0 = u < f ? u : u + 2 * half;
+  c1 = u + 1 < f ? u + 1 : u + 1 + 2 * half;
+  return false;
+}
+
+// The same item j of the heads h0, h0 + step, ... of one token.
+struct Heads {
+  const uint4* x;  // the token's rows, 16-byte chunks
+  uint4* out;
+  int heads, chunks;  // chunks of a head
+};
+
+__device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int pos, int j, int h0, int step) {
+  int c0, c1;
+  const bool turns = item_chunks(r, j, c0, c1);
+  constexpr int kAhead = 4;  // heads whose loads are under way together
+  float c[kPairs], s[kPairs];
+  bool have = false;
+  for (int h = h0; h < t.heads; h += kAhead * step) {
+    uint4 a[kAhead], b[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int hi = h + i * step;
+      if (hi < t.heads) {
+        a[i] = __ldcs(t.x + hi * t.chunks + c0);
+        b[i] = __ldcs(t.x + hi * t.chunks + c1);
+      }
+    }
+    if (turns && !have) {  // (under the loads)
+#pragma unroll
+      for (int i = 0; i < kPairs; i += 2) {
+        const ulonglong2 f = __ldg(reinterpret_cast<const ulonglong2*>(r.freqs + kPairs * j + i));
+        turn(pos, f.x, r.scale, c[i], s[i]);
+        turn(pos, f.y, r.scale, c[i + 1], s[i + 1]);
+      }
+      have = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int hi = h + i * step;
+      if (hi >= t.heads) break;
+      if (turns) {
+        if (r.interleaved) {
+          turn_neighbours(a[i], c, s);
+          turn_neighbours(b[i], c + 4, s + 4);
+        } else {
+          turn_halves(a[i], b[i], c, s);
+        }
+      }
+      t.out[hi * t.chunks + c0] = a[i];
+      t.out[hi * t.chunks + c1] = b[i];
+    }
+  }
+}
+
+// Threads that share a token's heads: all heads at once while the call is
+// small (its length is one thread's chain), else few, so that sines and cosines
+// serve several heads.
+inline int head_groups(int64_t tokens, int heads, int dim) {
+  const int64_t items = tokens * heads * (dim / 16);
+  if (items <= 152 * 2048) return heads;
+  return (heads + 7) / 8;
+}
+
+// Argument checks shared by the entry points.
+inline int check(const uint64_t* freqs, int first, int rot, int head_dim, float scale) {
+  if (rot < 16 || rot % 16 || first < 0 || first % 8 || first + static_cast<int64_t>(rot) > head_dim)
+    return MOE_ERR_UNSUPPORTED;
+  if (scale - scale != 0.0f) return MOE_ERR_ARG;
+  if (!freqs) return MOE_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(freqs) & 15) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+}  // namespace rope
+}  // namespace moe
