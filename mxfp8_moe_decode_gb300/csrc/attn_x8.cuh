@@ -141,36 +141,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One lane of a converged warp. (A branch on it, unlike one on the lane number,
-// tells the compiler that a single thread issues what follows; the instructions
-// that take uniform operands -- tcgen05, bulk copies -- otherwise cost it a
-// loop over the lanes each.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(yes));
-  return yes != 0;
-}
+using ptx::elect_one;
+using ptx::kWaitClocks;
 
-// Bounded wait for an mbarrier phase: about a second of SM clocks, or until the
-// CTA's abort flag is set (which a wait that runs out does). The clock is the
-// SM's own: a read of %globaltimer on the way costs about as much as the whole
-// wait for a product.
-constexpr long long kWaitClocks = 2000000000ll;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitClocks) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
+  return ptx::mbar_wait_clocks(bar, parity, abort);
 }
 
 // ---------------------------------------------------------------- work list
