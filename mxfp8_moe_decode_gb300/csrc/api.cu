@@ -654,20 +654,19 @@ void moe_destroy(moe_handle* h) {
 
 namespace moe {
 
-// Rows of 128-element blocks [rows][cols / 128][128] as a 3D tensor (element,
-// row, block), box = 128 elements x box_rows x box_blocks, 128-byte swizzle:
-// block after block, each the operand tile of one K stage.
-bool encode_blocks(CUtensorMap* tm, const void* base, bool e2m1, uint64_t cols, uint64_t rows, uint64_t row_bytes,
-                   uint32_t box_rows, uint32_t box_blocks) {
+// Byte rows in 128-byte blocks, `parts` such matrices part_bytes apart, as a 4D
+// tensor (byte, row, part, block); box = 128 bytes x box_rows x all parts x one
+// block, 128-byte swizzle: part after part, each the operand tile of a K stage.
+bool encode_blocks(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t parts,
+                   uint64_t part_bytes, uint32_t box_rows) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
-  const WeightType wt = e2m1 ? kE2M1Map : kE4M3Map;
-  const cuuint64_t dims[3] = {128, rows, cols / 128};
-  const cuuint64_t strides[2] = {row_bytes, 128 * wt.bytes_num / wt.bytes_den};
-  const cuuint32_t box[3] = {128, box_rows, box_blocks};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(tm, wt.dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[4] = {128, rows, parts, cols / 128};
+  const cuuint64_t strides[3] = {row_bytes, part_bytes, 128};
+  const cuuint32_t box[4] = {128, box_rows, parts, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -26,20 +26,26 @@ namespace {
 
 constexpr int kTileN = 128;      // weight rows of a tile (MMA M)
 constexpr int kMaxRows = 192;    // token rows of a tile (MMA N): two accumulators and the scales fit TMEM
-constexpr int kMaxStages = 16;
+constexpr int kMaxSlots = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kAProducers = 4;   // warps that issue the weights' copies
-constexpr int kBProducers = 3;   // warps that issue the rows' copies
-// warps: 0-3 epilogue, 4 MMA issuer, 5-7 scale images (weights, rows, rows' second part), 8.. producers
-constexpr int kWarps = 8 + kAProducers + kBProducers;
+constexpr int kStep = 2;         // K blocks (of 128) that a weight loader takes at once: 128 bytes of a row
+constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at once: 16 bytes of a row
+// Warps by role. Two warps that take the ring's slots in turn (issuers, rows'
+// copies) need an even number of slots, so that a slot's phases are all seen by
+// one of them: a warp that had missed one could take its parity for the one it
+// waits for.
+constexpr int kIssuer = 4, kCodesW = 6, kCodesX = 7, kCopyX = 9, kLoadW = 11, kWarps = 19;  // (epilogue: 0-3)
+constexpr int kLoaders = kWarps - kLoadW;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kABytes = kTileN * 128;
-constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block of 128
+constexpr uint32_t kRawBytes = kStep * kTileN * 64;
+constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct LinearParams {
-  CUtensorMap tm_w, tm_x[2];
+  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
+  const uint8_t* w;      // [N][K / 2]
   const uint8_t* wc;     // [N][K / 32]
   const uint8_t* xc[2];  // [M][K / 32]
   __nv_bfloat16* out;
@@ -49,18 +55,22 @@ struct LinearParams {
   int nt;                // token rows of a tile (a multiple of 16)
   int tiles_m, tasks;
   int parts;             // 1 (MXFP8 rows) or 2 (bf16 rows as hi and lo)
-  int blocks;            // K blocks of a stage (1 or 2)
-  int stages;            // ring slots
+  int stacked;           // two parts as columns of one product (few rows), else as two products
+  int cols;              // columns of a product (MMA N): nt, stacked 2 nt
+  int slots;             // of the ring: a K block's weights, rows and scale images each
+  int ahead;             // steps that a weight loader has under way (1, 2 or 4)
+  int issuers;           // 1 or 2, each with its own accumulators
+  int copiers;           // warps that copy rows (1 or 2)
   int split;             // CTAs (a cluster) that share a tile's K
-  uint32_t slot_bytes, off_img, slot_img, off_xchg, off_bar;
+  uint32_t off_b, slot_b, off_img, slot_img, off_raw, off_xchg, off_bar;
 };
 
 struct Bars {
-  uint64_t full[kMaxStages];   // weights, rows and scale images are there
-  uint64_t empty[kMaxStages];  // the stage's MMAs have read them
+  uint64_t full[kMaxSlots];   // a K block's weights, rows and images are there
+  uint64_t empty[kMaxSlots];  // its MMAs have read them
   uint64_t tfull[2], tempty[2];
-  uint64_t xfree;              // every CTA of the cluster has its exchange buffer free
-  uint64_t xfull;              // this CTA's exchange buffer is full
+  uint64_t efree;             // every CTA of the cluster has its exchange buffer free
+  uint64_t efull;             // this CTA's exchange buffer is full
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -69,15 +79,167 @@ struct Bars {
 using ptx::elect_one;
 using ptx::mbar_wait_clocks;
 
+// What a CTA goes through: its cluster's tiles, and of each the same K blocks
+// (its share of K, from an even one on).
+struct Work {
+  int first, step;  // tiles
+  int rank;
+  int nk, k0, k1;
+};
+
+__device__ __forceinline__ Work work_of(const LinearParams& p) {
+  Work w;
+  const int S = p.split;
+  w.rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
+  w.first = static_cast<int>(blockIdx.x) / S;
+  w.step = static_cast<int>(gridDim.x) / S;
+  w.nk = p.K / 128;
+  const int steps = (w.nk + kStep - 1) / kStep;
+  w.k0 = kStep * (steps * w.rank / S);
+  w.k1 = min(kStep * (steps * (w.rank + 1) / S), w.nk);
+  return w;
+}
+
+__device__ __forceinline__ int tile_n(const LinearParams& p, int t) { return t / p.tiles_m * kTileN; }
+__device__ __forceinline__ int tile_m(const LinearParams& p, int t) { return t % p.tiles_m * p.nt; }
+
+// A place in the ring, and the parity of its present phase.
+struct Slot {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n, int by = 1) {
+    at += by;
+    if (at >= n) {
+      at -= n;
+      phase ^= 1;
+    }
+  }
+};
+
+// 16 bytes of weights to shared memory; the 256 bytes around them come to L2 with them.
+__device__ __forceinline__ void copy_weights(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v2(uint32_t at, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
+}
+
+// Weights by one of the loader warps, its 16 rows of every tile: 128 bytes of a
+// row (two K blocks) to 8 lanes, 16 bytes each, `ahead` such steps on their way
+// to a place that only this thread reads again; then into the ring as the
+// tensor cores read E2M1 rows: 16 codes (8 bytes) in a unit of 16 bytes, whose
+// other half is not looked at, the units of a row of 128 permuted by the row
+// (128-byte swizzle).
+__device__ __forceinline__ void load_tiles(const LinearParams& p, const Work& w, Bars* bars, uint32_t sbase, int loader) {
+  const int lane = threadIdx.x & 31, sub = lane >> 3, half = (lane >> 2) & 1, c = lane & 3;
+  volatile int* abort = &bars->abort;
+  const long long pitch = p.K / 2;
+  const int row0 = 16 * loader + sub;
+  const int steps = (w.k1 - w.k0 + kStep - 1) / kStep;
+  const bool odd = (w.k1 - w.k0) & 1;  // the last step of a tile has one K block
+  const int tiles = w.first < p.tasks ? (p.tasks - 1 - w.first) / w.step + 1 : 0;
+  const int total = steps * tiles;
+  // rows 4 i further: the same permutation for i even, and for i odd
+  uint32_t at[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      at[i][u] = sbase + (row0 + 4 * i) * 128 + (((2 * c + u) ^ ((sub + 4 * i) & 7)) << 4);
+  const int ahead = p.ahead;
+  const uint32_t raw = sbase + p.off_raw + (loader * 128 + lane) * 16;  // + 16 KB a step, 512 every fourth row
+  const uint32_t raw_end = raw + ahead * kRawBytes;
+  // the next step to load
+  int lt = w.first, left_l = 0;
+  const uint8_t* src[4];
+  const auto load = [&](uint32_t dst) {
+    if (left_l == 0) {  // a tile's first
+      const int n0 = tile_n(p, lt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // (rows past the last repeat it)
+        src[i] = p.w + min(n0 + row0 + 4 * i, p.N - 1) * pitch + w.k0 * 64 + (lane & 7) * 16;
+      left_l = steps;
+      lt += w.step;
+    }
+    --left_l;
+    if (half == 0 || left_l > 0 || !odd) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy_weights(dst + i * 512, src[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) src[i] += kStep * 64;
+  };
+  for (int j = 0; j < ahead; ++j) {
+    if (j < total) load(raw + j * kRawBytes);
+    copy_commit();
+  }
+  __syncthreads();  // the barriers are there
+  if (p.split > 1) ptx::cluster_arrive();
+  Slot a, b;  // of the step's first and second K block
+  b.next(p.slots);
+  int left = steps;
+  uint32_t from = raw;
+  const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full);
+  for (int i = 0; i < total; ++i) {
+    --left;
+    const bool two = left > 0 || !odd;
+    if (ahead == 4)
+      copy_wait<3>();
+    else if (ahead == 2)
+      copy_wait<1>();
+    else
+      copy_wait<0>();
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
+                   : "r"(from + q * 512)
+                   : "memory");
+    bool ok = mbar_wait_clocks(empty0 + a.at * 8, a.phase ^ 1, abort);
+    if (two) ok = ok && mbar_wait_clocks(empty0 + b.at * 8, b.phase ^ 1, abort);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    if (half == 0 || two) {
+      const uint32_t to = (half ? b.at : a.at) * kABytes;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        st_shared_v2(to + (q >> 1) * 1024 + at[q & 1][0], v[q].x, v[q].y);
+        st_shared_v2(to + (q >> 1) * 1024 + at[q & 1][1], v[q].z, v[q].w);
+      }
+    }
+    __syncwarp();
+    if (elect_one()) {
+      ptx::mbar_arrive(full0 + a.at * 8);
+      if (two) ptx::mbar_arrive(full0 + b.at * 8);
+    }
+    if (i + ahead < total) load(from);  // (what was there is in the ring)
+    copy_commit();
+    from += kRawBytes;
+    if (from == raw_end) from = raw;
+    if (left == 0) left = steps;
+    a.next(p.slots, two ? 2 : 1);
+    b.next(p.slots, two ? 2 : 1);
+  }
+  copy_wait<0>();
+}
+
 // 4 K blocks' codes of one row (word j: the block 4 g + j), as 16 bytes where a
-// row's codes are 16-byte aligned.
+// row's codes are 16-byte aligned; the 128 bytes around them come to L2 too.
 __device__ __forceinline__ uint4 load_codes(const uint8_t* row, int g, int nk, bool wide) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (wide) {
-    v = __ldg(reinterpret_cast<const uint4*>(row) + g);
+    asm volatile("ld.global.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(reinterpret_cast<const uint4*>(row) + g));
   } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + 4 * g;
-    const int n = nk - 4 * g;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + kGroup * g;
+    const int n = nk - kGroup * g;
     v.x = __ldg(w);
     if (n > 1) v.y = __ldg(w + 1);
     if (n > 2) v.z = __ldg(w + 2);
@@ -86,143 +248,212 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* row, int g, int nk, b
   return v;
 }
 
+template <int kImages>
+struct Codes {
+  uint4 v[kImages][4];
+};
+
+template <int kImages, bool kRows>
+__device__ __forceinline__ void load_group(const LinearParams& p, const Work& w, const uint8_t* codes, bool wide,
+                                           int t, int g, Codes<kImages>& c) {
+  const int lane = threadIdx.x & 31;
+  const int r0 = kRows ? tile_m(p, t) : tile_n(p, t);
+  const int rows = min((kRows ? p.M : p.N) - r0, kRows ? p.nt : kTileN);
+  const long long pitch = p.K / 32;
+#pragma unroll
+  for (int i = 0; i < kImages; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      int r = 128 * i + 32 * q + lane;
+      const uint8_t* from = codes;
+      if (kRows && p.stacked && r >= p.nt) {  // lo behind hi
+        r -= p.nt;
+        from = p.xc[1];
+      }
+      c.v[i][q] = make_uint4(0, 0, 0, 0);
+      if (r < rows) c.v[i][q] = load_codes(from + (r0 + r) * pitch, g, w.nk, wide);
+    }
+}
+
 __device__ __forceinline__ uint32_t word(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// Scale images by one warp: a K block's codes as tcgen05.cp reads them: lane
+// i's 16 bytes hold the 4 codes each of the rows i, 32 + i, 64 + i, 96 + i.
+// Codes are loaded 4 K blocks at a time, one such group ahead. kRows: of the
+// rows' part `part`, else the weights'.
+template <int kImages, bool kRows>
+__device__ __forceinline__ void scale_images(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int part) {
+  const int lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  const uint8_t* codes = kRows ? p.xc[part] : p.wc;
+  const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(codes) & 15) == 0;  // (the workspace's are aligned)
+  uint8_t* base = smem + p.off_img + (kRows ? 1 + part * kImages : 0) * kImg + lane * 16;
+  const int g0 = w.k0 / kGroup;
+  Codes<kImages> next;
+  if (w.first < p.tasks) load_group<kImages, kRows>(p, w, codes, wide, w.first, g0, next);
+  __syncthreads();  // the barriers are there
+  if (p.split > 1) ptx::cluster_arrive();
+  Slot slot;
+  for (int t = w.first; t < p.tasks; t += w.step) {
+    Codes<kImages> now;
+    for (int k = w.k0; k < w.k1; ++k) {
+      const int j = k % kGroup;
+      if (k == w.k0 || j == 0) {
+        now = next;
+        if (k - j + kGroup < w.k1)
+          load_group<kImages, kRows>(p, w, codes, wide, t, k / kGroup + 1, next);
+        else if (t + w.step < p.tasks)
+          load_group<kImages, kRows>(p, w, codes, wide, t + w.step, g0, next);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort))) return;
+      uint8_t* dst = base + slot.at * p.slot_img;
+#pragma unroll
+      for (int m = 0; m < kImages; ++m)
+        *reinterpret_cast<uint4*>(dst + m * kImg) =
+            make_uint4(word(now.v[m][0], j), word(now.v[m][1], j), word(now.v[m][2], j), word(now.v[m][3], j));
+      __syncwarp();
+      if (elect_one()) ptx::mbar_arrive(ptx::smem_u32(&bars->full[slot.at]));
+      slot.next(p.slots);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
+  const uint32_t sbase = ptx::smem_u32(smem);
   Bars* bars = reinterpret_cast<Bars*>(smem + p.off_bar);
   volatile int* abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
-  const int S = p.split, R = p.stages;
-  const int rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
-  const int cluster = static_cast<int>(blockIdx.x) / S, clusters = static_cast<int>(gridDim.x) / S;
-  const int nk = p.K / 128, steps = (nk + p.blocks - 1) / p.blocks;
-  const int s0 = steps * rank / S, s1 = steps * (rank + 1) / S;  // this CTA's stages of a tile
-  const int himg = p.nt > 128 ? 2 : 1;                           // scale images of a rows' part
+  const int S = p.split;
+  const Work w = work_of(p);
+  const int himg = p.cols > 128 ? 2 : 1;            // scale images of a product's columns
+  const int products = p.stacked ? 1 : p.parts;     // of a K block
 
-  if (tid == 0) {
-    for (int i = 0; i < R; ++i) {
-      ptx::mbar_init(bar(bars->full[i]), 2 + 2 * p.parts);  // copies and images of the weights and each part
-      ptx::mbar_init(bar(bars->empty[i]), 1);
+  if (warp == 0) {
+    if (lane < kMaxSlots) {
+      ptx::mbar_init(bar(bars->full[lane]), kLoaders + 1 + 1 + products);  // weights, rows, images of both
+      ptx::mbar_init(bar(bars->empty[lane]), 1);
+    } else if (lane < 10) {
+      ptx::mbar_init(bar(bars->tfull[lane - 8]), p.issuers);
+      ptx::mbar_init(bar(bars->tempty[lane - 8]), 4);
+    } else if (lane == 10) {
+      ptx::mbar_init(bar(bars->efree), S);
+    } else if (lane == 11) {
+      ptx::mbar_init(bar(bars->efull), 4 * S);
+    } else if (lane == 12) {
+      ptx::mbar_init(bar(bars->drain), p.issuers);
+    } else if (lane == 13) {
+      bars->abort = 0;
     }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(bars->tfull[i]), 1);
-      ptx::mbar_init(bar(bars->tempty[i]), 4);
-    }
-    ptx::mbar_init(bar(bars->xfree), S);
-    ptx::mbar_init(bar(bars->xfull), 4 * S);
-    ptx::mbar_init(bar(bars->drain), 1);
-    bars->abort = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&p.tm_w);
-    ptx::prefetch_tmap(&p.tm_x[0]);
-    if (p.parts > 1) ptx::prefetch_tmap(&p.tm_x[1]);
-  }
-  if (warp == 4) {
+  } else if (warp == kIssuer) {
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem), kTmemCols);
     ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  } else if (warp == kCopyX && elect_one()) {
+    ptx::prefetch_tmap(&p.tm_x);
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  if (S > 1) ptx::cluster_sync();  // the others' barriers are initialised
-  const uint32_t tmem = bars->tmem;
+  __syncwarp();
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  // (every branch waits for the barriers' initialisation, and in a cluster says
+  // that its CTA's are there)
+  if (warp >= kLoadW) {
+    load_tiles(p, w, bars, sbase, warp - kLoadW);
+  } else if (warp == kCodesW) {
+    scale_images<1, false>(p, w, bars, smem, 0);
+  } else if (warp >= kCodesX && warp < kCodesX + products) {
+    if (himg == 1)
+      scale_images<1, true>(p, w, bars, smem, warp - kCodesX);
+    else
+      scale_images<2, true>(p, w, bars, smem, warp - kCodesX);
+  } else {
+    __syncthreads();
+    if (S > 1) ptx::cluster_arrive();
+    ptx::tc_fence_after();
+  }
 
-  if (warp >= 8) {
-    // ------------------------------------------------------------ producers
-    // The stages go to the warps of a kind in turn, to no more warps than the
-    // ring has slots: the slots are freed in order, and a warp has seen that of
-    // its last stage, at most R stages ago, free, so none comes two phases late
-    // to a slot (and takes its parity for the one it wants).
-    const bool is_a = warp < 8 + kAProducers;
-    const int who = is_a ? warp - 8 : warp - 8 - kAProducers, of = min(is_a ? kAProducers : kBProducers, R);
-    if (who < of && elect_one()) {
-      const uint64_t policy = is_a ? ptx::policy_evict_first() : ptx::policy_evict_last();
-      const uint32_t part_bytes = static_cast<uint32_t>(p.nt) * 128u * p.blocks;
-      // (a 4-bit box counts its global bytes, half of what it fills)
-      const uint32_t bytes = is_a ? kABytes / 2 * p.blocks : part_bytes;
-      int it = 0;
+  if (warp >= kCopyX && warp < kCopyX + p.copiers) {
+    // ------------------------------------------------------------ rows' copies
+    if (elect_one()) {
+      const uint64_t policy = ptx::policy_evict_last();
+      const int me = warp - kCopyX;
+      int turn = 0;
+      Slot slot;
       bool ok = true;
-      for (int t = cluster; ok && t < p.tasks; t += clusters) {
-        const int n0 = t / p.tiles_m * kTileN, m0 = t % p.tiles_m * p.nt;
-        for (int s = s0; s < s1; ++s, ++it) {
-          if (it % of != who) continue;
-          const int slot = it % R;
-          if (!mbar_wait_clocks(bar(bars->empty[slot]), ((it / R) & 1) ^ 1, abort)) {
+      for (int t = w.first; ok && t < p.tasks; t += w.step) {
+        const int row = tile_m(p, t);
+        for (int k = w.k0; k < w.k1; ++k, slot.next(p.slots)) {
+          const bool mine = turn == me;
+          if (++turn == p.copiers) turn = 0;
+          if (!mine) continue;
+          if (!mbar_wait_clocks(bar(bars->empty[slot.at]), slot.phase ^ 1, abort)) {
             ok = false;
             break;
           }
-          const uint32_t full = bar(bars->full[slot]);
-          const uint32_t dst = ptx::smem_u32(smem) + slot * p.slot_bytes;
-          if (is_a) {
-            ptx::mbar_arrive_expect_tx(full, bytes);
-            ptx::tma_load_3d(dst, &p.tm_w, 0, n0, s * p.blocks, full, policy);
-          } else {
-            for (int h = 0; h < p.parts; ++h) {
-              ptx::mbar_arrive_expect_tx(full, bytes);
-              ptx::tma_load_3d(dst + p.blocks * kABytes + h * part_bytes, &p.tm_x[h], 0, m0, s * p.blocks, full,
-                               policy);
-            }
-          }
+          const uint32_t full = bar(bars->full[slot.at]);
+          ptx::mbar_arrive_expect_tx(full, p.slot_b);
+          ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, row, 0, k, full, policy);
         }
       }
     }
     __syncwarp();
-  } else if (warp == 4) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp >= kIssuer && warp < kIssuer + p.issuers) {
+    // ------------------------------------------------------------ MMA issuers
     if (elect_one()) {
-      const uint32_t sf0 = tmem + 2 * p.nt, sf_slot = p.blocks * (4 + 4 * p.parts * himg);
-      const uint32_t part_bytes = static_cast<uint32_t>(p.nt) * 128u * p.blocks;
-      uint32_t idesc[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) idesc[k] = ptx::idesc_mxf8(p.nt, k, ptx::kFmtE2M1);
-      int slot = 0, round = 0, lt = 0;
+      const uint32_t me = warp - kIssuer, tmem = bars->tmem;
+      // A K block's scale columns in TMEM, by its slot: 4 of the weights, then 4
+      // himg of each product's rows. (The products take them from a column that
+      // is a multiple of 4 only.)
+      const uint32_t sfx = 4 * himg, sf_slot = 4 + products * sfx;
+      const uint32_t sf0 = tmem + 2 * p.issuers * p.cols;
+      const uint32_t part_bytes = static_cast<uint32_t>(p.nt) * 128u;
+      const uint32_t idesc = ptx::idesc_mxf8(p.cols, 0, ptx::kFmtE2M1), idesc_k = ptx::idesc_mxf8(0, 1, 0) - ptx::idesc_mxf8(0, 0, 0);
+      uint32_t turn = 0, acc = 0, acc_phase = 1;
+      Slot slot;
       bool ok = true;
-      for (int t = cluster; ok && t < p.tasks; t += clusters, ++lt) {
-        const int acc = lt & 1;
-        if (!mbar_wait_clocks(bar(bars->tempty[acc]), ((lt >> 1) & 1) ^ 1, abort)) break;
+      for (int t = w.first; ok && t < p.tasks; t += w.step) {
+        if (!mbar_wait_clocks(bar(bars->tempty[acc]), acc_phase, abort)) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + acc * p.nt;
+        const uint32_t d = tmem + (acc * p.issuers + me) * p.cols;
         uint32_t some = 0;
-        for (int s = s0; s < s1; ++s) {
-          if (!mbar_wait_clocks(bar(bars->full[slot]), round & 1, abort)) {
+        for (int k = w.k0; k < w.k1; ++k, slot.next(p.slots)) {
+          const bool mine = turn == me;
+          if (++turn == static_cast<uint32_t>(p.issuers)) turn = 0;
+          if (!mine) continue;
+          if (!mbar_wait_clocks(bar(bars->full[slot.at]), slot.phase, abort)) {
             ok = false;
             break;
           }
+          // The weights and images that other warps wrote, to the tensor cores'
+          // view of shared memory.
+          ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
-          const uint32_t a = ptx::smem_u32(smem) + slot * p.slot_bytes;
-          const uint32_t b = a + p.blocks * kABytes;
-          uint32_t img = ptx::smem_u32(smem) + p.off_img + slot * p.slot_img;
-          uint32_t sf = sf0 + slot * sf_slot;
-          for (int k = 0; k < p.blocks; ++k) {
-            ptx::tc_cp_32x128b_x4(sf, ptx::sdesc_rows16(img));
-            for (int h = 0; h < p.parts * himg; ++h)
-              ptx::tc_cp_32x128b_x4(sf + 4 + 4 * h, ptx::sdesc_rows16(img + (1 + h) * kImg));
-            for (int h = 0; h < p.parts; ++h) {
+          const uint32_t a = sbase + slot.at * kABytes;
+          const uint32_t b = sbase + p.off_b + slot.at * p.slot_b;
+          const uint32_t img = sbase + p.off_img + slot.at * p.slot_img;
+          const uint32_t sfa = sf0 + slot.at * sf_slot;
+          ptx::tc_cp_32x128b_x4(sfa, ptx::sdesc_rows16(img));
+          for (int h = 0; h < products; ++h) {
+            const uint32_t sx = sfa + 4 + h * sfx;
+            for (int i = 0; i < himg; ++i)
+              ptx::tc_cp_32x128b_x4(sx + 4 * i, ptx::sdesc_rows16(img + (1 + h * himg + i) * kImg));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                ptx::tc_mma_mxf8(d, ptx::sdesc_k128_sw128(a + k * kABytes + 32 * kk),
-                                 ptx::sdesc_k128_sw128(b + h * part_bytes + k * p.nt * 128 + 32 * kk), idesc[kk], sf,
-                                 sf + 4 + 4 * h * himg, some);
-                some = 1;
-              }
+            for (int kk = 0; kk < 4; ++kk) {
+              ptx::tc_mma_mxf8(d, ptx::sdesc_k128_sw128(a + 32 * kk), ptx::sdesc_k128_sw128(b + h * part_bytes + 32 * kk),
+                               idesc + kk * idesc_k, sfa, sx, some);
+              some = 1;
             }
-            sf += 4 + 4 * p.parts * himg;
-            img += (1 + p.parts * himg) * kImg;
           }
-          ptx::tc_commit(bar(bars->empty[slot]));
-          if (++slot == R) {
-            slot = 0;
-            ++round;
-          }
+          ptx::tc_commit(bar(bars->empty[slot.at]));
         }
         if (ok) ptx::tc_commit(bar(bars->tfull[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
       }
       // everything this thread issued has completed once drain fires
       ptx::tc_commit(bar(bars->drain));
@@ -230,72 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       mbar_wait_clocks(bar(bars->drain), 0, &never);
     }
     __syncwarp();
-  } else if (warp >= 5) {
-    // ------------------------------------------------------------ scale images
-    // Image of a K block: lane i's 16 bytes hold the 4 codes of the rows i, 32 +
-    // i, 64 + i, 96 + i. Codes are loaded 4 K blocks at a time, one such group
-    // ahead.
-    const int part = warp - 6;  // -1: the weights
-    if (part < p.parts) {
-      const uint8_t* codes = part < 0 ? p.wc : p.xc[part];
-      const int count = part < 0 ? p.N : p.M, images = part < 0 ? 1 : himg, pitch = p.K / 32;
-      const int tile = part < 0 ? kTileN : p.nt;
-      const bool wide = pitch % 16 == 0 && (reinterpret_cast<uintptr_t>(codes) & 15) == 0;
-      const uint32_t off = part < 0 ? 0 : (1 + part * himg) * kImg;
-      int slot = 0, round = 0;
-      bool ok = true;
-      for (int t = cluster; ok && t < p.tasks; t += clusters) {
-        const int r0 = part < 0 ? t / p.tiles_m * kTileN : t % p.tiles_m * p.nt;
-        const auto fetch = [&](uint4 (&v)[2][4], int g) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int r = 128 * i + 32 * c + lane;
-              v[i][c] = make_uint4(0, 0, 0, 0);
-              if (i < images && r < tile && r0 + r < count && 4 * g < nk)
-                v[i][c] = load_codes(codes + static_cast<long long>(r0 + r) * pitch, g, nk, wide);
-            }
-        };
-        uint4 cur[2][4], nxt[2][4];
-        fetch(nxt, s0 * p.blocks / 4);
-        for (int s = s0; s < s1; ++s) {
-          const int k0 = s * p.blocks;
-          if (s == s0 || k0 % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) cur[i][c] = nxt[i][c];
-            fetch(nxt, k0 / 4 + 1);
-          }
-          if (!__all_sync(0xffffffffu, mbar_wait_clocks(bar(bars->empty[slot]), (round & 1) ^ 1, abort))) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = smem + p.off_img + slot * p.slot_img + off + lane * 16;
-          for (int k = 0; k < p.blocks; ++k) {
-            const int j = (k0 + k) & 3;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (i < images)
-                *reinterpret_cast<uint4*>(dst + i * kImg) =
-                    make_uint4(word(cur[i][0], j), word(cur[i][1], j), word(cur[i][2], j), word(cur[i][3], j));
-            dst += (1 + p.parts * himg) * kImg;
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) ptx::mbar_arrive(bar(bars->full[slot]));
-          if (++slot == R) {
-            slot = 0;
-            ++round;
-          }
-        }
-      }
-    }
-  } else {
+  } else if (warp < kIssuer) {
     // ------------------------------------------------------------ epilogue
     // Warp q holds the tile's weight rows 32 q .. 32 q + 31, one a lane.
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
     // A warp whose wait ran out goes on to the next tile's barrier, where all
     // four give up together.
     const auto all_ok = [](bool ok) {
@@ -308,22 +476,40 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           : "memory");
       return all != 0;
     };
+    const uint32_t lanes = bars->tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int per = (p.nt / 4 + S - 1) / S;  // groups of 4 columns that a CTA of the cluster sums
+    const uint32_t xchg = sbase + p.off_xchg + tid * 16;
     int lt = 0;
     bool ok = true;
-    for (int t = cluster; t < p.tasks; t += clusters, ++lt) {
-      const int n = t / p.tiles_m * kTileN + tid, m0 = t % p.tiles_m * p.nt;
+    if (S > 1) ptx::cluster_wait();  // (every warp arrived; the others wait at the end)
+    for (int t = w.first; t < p.tasks; t += w.step, ++lt) {
+      const int n = tile_n(p, t) + tid, m0 = tile_m(p, t);
       const int cols = min(p.nt, p.M - m0);
       const int acc = lt & 1;
       ok = ok && __all_sync(0xffffffffu, mbar_wait_clocks(bar(bars->tfull[acc]), (lt >> 1) & 1, abort));
       if (S > 1 ? !all_ok(ok) : !ok) break;
       ptx::tc_fence_after();
-      const uint32_t d = tmem + lanes + acc * p.nt;
+      // the issuers' accumulators (one, if the tile had a single K block: its issuer's)
+      const uint32_t d0 = lanes + acc * p.issuers * p.cols;
+      const bool two = p.issuers > 1 && w.k1 - w.k0 > 1;
+      const uint32_t d = d0 + (p.issuers > 1 && !two ? (lt & 1) * p.cols : 0);
+      const auto load = [&](int c0, float* v) {
+        ptx::tmem_ld_32x32b_x16(d + c0, v);
+        ptx::tmem_wait_ld();
+        // the other issuer's sums, and lo's
+        for (int at = p.stacked ? p.nt : p.cols; at < (two ? 2 : 1) * p.cols; at += p.stacked ? p.nt : p.cols) {
+          float u[16];
+          ptx::tmem_ld_32x32b_x16(d + at + c0, u);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += u[j];
+        }
+      };
       __nv_bfloat16* out = p.out + static_cast<long long>(m0) * p.ldo + n;
       if (S == 1) {
         for (int c0 = 0; c0 < cols; c0 += 16) {
           float v[16];
-          ptx::tmem_ld_32x32b_x16(d + c0, v);
-          ptx::tmem_wait_ld();
+          load(c0, v);
           if (n < p.N) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -335,45 +521,59 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         if (lane == 0) ptx::mbar_arrive(bar(bars->tempty[acc]));
         continue;
       }
-      // The tile's column j is summed by the CTA j % S. Every CTA says that its
-      // buffer is free (its last tile's sums are read; where the buffer lies
-      // over the ring, all MMAs are done too), sends its parts of the columns to
-      // their CTAs, and adds up those it gets in the order of the ranks.
-      if (tid < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->xfree), tid));
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->xfree), lt & 1, abort));
+      // Columns 4 c .. 4 c + 3 of the tile are summed by the CTA c % S. Every CTA
+      // says that its buffer is free (its last tile's sums are read; where the
+      // buffer lies over the ring, all MMAs are done too), sends its parts of
+      // the columns to their CTAs, and adds up those it gets in the order of the ranks.
+      if (tid < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), tid));
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efree), lt & 1, abort));
       if (!ok) continue;
-      const int per = (p.nt + S - 1) / S;
-      const uint32_t xchg = ptx::smem_u32(smem) + p.off_xchg;
+      int owner = 0;
+      uint32_t at = xchg + w.rank * per * 2048;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
-        ptx::tmem_ld_32x32b_x16(d + c0, v);
-        ptx::tmem_wait_ld();
+        load(c0, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int c = c0 + j;
-          if (c < cols)
-            ptx::st_cluster_f32(ptx::cluster_addr(xchg + ((rank * per + c / S) * 128 + tid) * 4, c % S), v[j]);
+        for (int j = 0; j < 16; j += 4) {
+          if (c0 + j < cols) {
+            ptx::st_cluster_v4(ptx::cluster_addr(at, owner), v[j], v[j + 1], v[j + 2], v[j + 3]);
+            if (++owner == S) {
+              owner = 0;
+              at += 2048;
+            }
+          }
         }
       }
       ptx::tc_fence_before();
       ptx::fence_cluster();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars->tempty[acc]));
-      if (lane < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->xfull), lane));
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->xfull), lt & 1, abort));
+      if (lane < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efull), lane));
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efull), lt & 1, abort));
       if (!ok) continue;
-      const float* part = reinterpret_cast<const float*>(smem + p.off_xchg) + tid;
       if (n < p.N) {
-        for (int i = 0; i * S + rank < cols; ++i) {
-          float sum = part[i * 128];
-          for (int r = 1; r < S; ++r) sum += part[(r * per + i) * 128];
-          out[(i * S + rank) * p.ldo] = __float2bfloat16_rn(sum);
+        const float4* part = reinterpret_cast<const float4*>(smem + p.off_xchg) + tid;
+        for (int c = 4 * w.rank; c < cols; c += 4 * S, part += 128) {
+          float4 sum = part[0];
+          for (int r = 1; r < S; ++r) {
+            const float4 u = part[r * per * 128];
+            sum.x += u.x;
+            sum.y += u.y;
+            sum.z += u.z;
+            sum.w += u.w;
+          }
+          __nv_bfloat16* o = out + c * p.ldo;
+          o[0] = __float2bfloat16_rn(sum.x);
+          if (c + 1 < cols) o[p.ldo] = __float2bfloat16_rn(sum.y);
+          if (c + 2 < cols) o[2 * p.ldo] = __float2bfloat16_rn(sum.z);
+          if (c + 3 < cols) o[3 * p.ldo] = __float2bfloat16_rn(sum.w);
         }
       }
     }
   }
 
   // ------------------------------------------------------------ teardown
+  if (S > 1 && warp >= kIssuer) ptx::cluster_wait();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort && tid == 0) {
@@ -385,11 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kIssuer) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTmemCols);
+    ptx::tmem_dealloc(bars->tmem, kTmemCols);
   }
-  if (S > 1) ptx::cluster_sync();  // nobody writes here any more
+  if (S > 1) {  // nobody writes here any more
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+  }
 }
 
 // ---------------------------------------------------------------- bf16 rows as two MXFP8 rows
@@ -497,7 +700,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   if (K < 128 || K % 128 || K > (1 << 16)) return MOE_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MOE_OK;
   if (!x || !w || !w_codes || !out) return MOE_ERR_ARG;
-  if (!aligned(x, 16) || !aligned(w, 32) || !aligned(w_codes, 4) || !aligned(out, 2) || !aligned(x_codes, 4) ||
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(w_codes, 4) || !aligned(out, 2) || !aligned(x_codes, 4) ||
       !aligned(status, 4) || !aligned(workspace, 16) || ldx % (x_codes ? 16 : 8))
     return MOE_ERR_ALIGN;
   if (ldx < K || ldo < N) return MOE_ERR_ARG;
@@ -511,6 +714,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   LinearParams p = {};
+  p.w = w;
   p.wc = w_codes;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
@@ -524,15 +728,24 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const int64_t tasks = static_cast<int64_t>((N + kTileN - 1) / kTileN) * p.tiles_m;
   if (tasks > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
   p.tasks = static_cast<int>(tasks);
-  p.blocks = p.nt * p.parts <= 32 ? 2 : 1;
-  const int steps = (K / 128 + p.blocks - 1) / p.blocks;
+  // bf16 rows: a product of 32 to 64 columns takes the time of one of 16, so few
+  // rows' two parts are columns of one product; the products of more are two
+  // that share their scales' copies and weights.
+  p.stacked = p.parts == 2 && p.nt <= 64;
+  p.cols = p.stacked ? 2 * p.nt : p.nt;
+  p.issuers = p.cols <= 96 ? 2 : 1;  // (their accumulators fit TMEM; the time of wider products hides the issue)
+  const int himg = p.cols > 128 ? 2 : 1, products = p.stacked ? 1 : p.parts;
+  p.slot_b = p.parts * p.nt * 128u;
+  p.slot_img = (1 + products * himg) * kImg;
+  const uint32_t fixed = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
+  const int steps = (K / 128 + kStep - 1) / kStep;
 
   // CTAs that share a tile's K: as many as the device holds at once over all
   // tiles, while each has some stages to itself; shares of one task a cluster
   // only, or with an exchange buffer beside the ring.
   int split = 1, clusters = max_clusters(device, 1);
   if (clusters == 0) return MOE_ERR_CUDA;
-  const auto cost = [&](int s, int c) { return (tasks + c - 1) / c * ((steps + s - 1) / s + (s > 1 ? 4 : 2)); };
+  const auto cost = [&](int s, int c) { return (tasks + c - 1) / c * ((steps + s - 1) / s * kStep + (s > 1 ? 6 : 3)); };
   int64_t best = cost(1, clusters);
   for (int s = 2; s <= kMaxCluster && s <= steps; ++s) {
     const int c = max_clusters(device, s);
@@ -545,21 +758,23 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   }
   p.split = split;
   clusters = static_cast<int>(std::min<int64_t>(clusters, tasks));
-  const int himg = p.nt > 128 ? 2 : 1;
-  p.slot_bytes = p.blocks * (kABytes + p.parts * p.nt * 128u);
-  p.slot_img = p.blocks * (1 + p.parts * himg) * kImg;
-  const uint32_t xchg = split > 1 ? static_cast<uint32_t>((p.nt + split - 1) / split * split) * 512u : 0;
-  const bool over = tasks <= clusters;  // the exchange buffer lies over the ring
-  const uint32_t room = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64 - (over ? 0 : xchg);
-  const uint32_t by_smem = room / (p.slot_bytes + p.slot_img);
-  const uint32_t by_tmem = (kTmemCols - 2 * p.nt) / (p.blocks * (4 + 4 * p.parts * himg));
-  p.stages = static_cast<int>(std::min<uint32_t>({by_smem, by_tmem, kMaxStages}));
-  p.off_img = p.stages * p.slot_bytes;
-  p.off_xchg = over ? 0 : p.off_img + p.stages * p.slot_img;
-  p.off_bar = p.off_img + p.stages * p.slot_img + (over ? 0 : xchg);
-  if (over && xchg > p.off_bar) return MOE_ERR_UNSUPPORTED;
+  const uint32_t xchg = split > 1 ? static_cast<uint32_t>((p.nt / 4 + split - 1) / split * split) * 2048u : 0;
+  const bool over = tasks <= clusters;  // the exchange buffer lies over the rings
+  // few rows wait for the weights from HBM, more for the tensor cores
+  p.ahead = p.cols <= 128 ? 4 : p.slot_b <= 32768 ? 2 : 1;
+  const uint32_t room = fixed - (over ? 0 : xchg) - p.ahead * kRawBytes;
+  p.slots = static_cast<int>(std::min<uint32_t>(room / (kABytes + p.slot_b + p.slot_img), kMaxSlots));
+  if (p.slots > 4 || p.issuers > 1) p.slots &= ~1;
+  p.copiers = p.slots % 2 == 0 ? 2 : 1;
+  if (p.slots < 2) return MOE_ERR_UNSUPPORTED;  // (no size reaches this)
+  p.off_b = p.slots * kABytes;
+  p.off_img = p.off_b + p.slots * p.slot_b;
+  p.off_raw = p.off_img + p.slots * p.slot_img;
+  p.off_xchg = over ? 0 : p.off_raw + p.ahead * kRawBytes;
+  p.off_bar = p.off_raw + p.ahead * kRawBytes + (over ? 0 : xchg);
+  if (over && xchg > p.off_img) return MOE_ERR_UNSUPPORTED;
 
-  const uint8_t* xs[2] = {static_cast<const uint8_t*>(x), nullptr};
+  const uint8_t* rows = static_cast<const uint8_t*>(x);
   int64_t row_bytes = ldx;
   p.xc[0] = x_codes;
   if (!x_codes) {
@@ -573,10 +788,8 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
     q.x8[1] = ws + static_cast<size_t>(M) * K;
     q.xc[0] = ws + 2 * static_cast<size_t>(M) * K;
     q.xc[1] = q.xc[0] + split_codes(M, K);
-    for (int h = 0; h < 2; ++h) {
-      xs[h] = q.x8[h];
-      p.xc[h] = q.xc[h];
-    }
+    for (int h = 0; h < 2; ++h) p.xc[h] = q.xc[h];
+    rows = ws;
     row_bytes = K;
     const cudaError_t e = launch_pdl(split_kernel, dim3(static_cast<unsigned>((q.octets + 255) / 256)), dim3(256), 0, st, q);
     if (e != cudaSuccess) {
@@ -584,9 +797,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
       return MOE_ERR_CUDA;
     }
   }
-  if (!encode_blocks(&p.tm_w, w, true, K, N, K / 2, kTileN, p.blocks)) return MOE_ERR_CUDA;
-  for (int h = 0; h < p.parts; ++h)
-    if (!encode_blocks(&p.tm_x[h], xs[h], false, K, M, row_bytes, p.nt, p.blocks)) return MOE_ERR_CUDA;
+  if (!encode_blocks(&p.tm_x, rows, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K, p.nt)) return MOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
