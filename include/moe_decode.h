@@ -591,7 +591,7 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
 
 /*
  * Products with 4-bit weights: out[m, n] = bf16(sum_k x[m, k] * w[n, k]).
- *  w        e2m1x2 u8 [N, K/2] (device, contiguous, 16-byte aligned): column 2j
+ *  w        e2m1x2 u8 [N, K/2] (device, contiguous, 32-byte aligned): column 2j
  *           in the low nibble of byte j of a row, as the routed experts' rows of
  *           MOE_ROUTED_E2M1; w_codes u8 [N, K/32] (4-byte aligned): its E8M0 codes,
  *           one per row per 32 columns (255 stands for NaN)

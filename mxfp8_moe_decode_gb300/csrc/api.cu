@@ -654,19 +654,23 @@ void moe_destroy(moe_handle* h) {
 
 namespace moe {
 
-// Byte rows in 128-byte blocks, `parts` such matrices part_bytes apart, as a 4D
-// tensor (byte, row, part, block); box = 128 bytes x box_rows x all parts x one
-// block, 128-byte swizzle: part after part, each the operand tile of a K stage.
-bool encode_blocks(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t parts,
-                   uint64_t part_bytes, uint32_t box_rows) {
+// Rows in blocks of 128 elements (bytes, or E2M1 codes of 4 bits), `parts` such
+// matrices part_bytes apart, as a tensor (element, row, part, block), with parts
+// = 0 without that dimension; box = 128 elements x box_rows x box_parts x one
+// block, 128-byte swizzle: part after part, each an operand tile of a K stage.
+bool encode_blocks(CUtensorMap* tm, const void* base, bool e2m1, uint64_t cols, uint64_t rows, uint64_t row_bytes,
+                   uint32_t parts, uint64_t part_bytes, uint32_t box_rows, uint32_t box_parts) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[4] = {128, rows, parts, cols / 128};
-  const cuuint64_t strides[3] = {row_bytes, part_bytes, 128};
-  const cuuint32_t box[4] = {128, box_rows, parts, 1};
+  const WeightType wt = e2m1 ? kE2M1Map : kE4M3Map;
+  const cuuint64_t block_bytes = 128 * wt.bytes_num / wt.bytes_den;
+  const int rank = parts > 0 ? 4 : 3;
+  const cuuint64_t dims[4] = {128, rows, parts > 0 ? parts : cols / 128, cols / 128};
+  const cuuint64_t strides[3] = {row_bytes, parts > 0 ? part_bytes : block_bytes, block_bytes};
+  const cuuint32_t box[4] = {128, box_rows, box_parts, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(tm, wt.dt, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

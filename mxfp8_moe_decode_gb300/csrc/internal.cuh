@@ -266,8 +266,8 @@ cudaError_t expert_occupancy(int fp4, int* per_sm);
 size_t expert_smem_bytes(int phase);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t s);
 cudaError_t launch_sfa_pack(const SfaPackParams& p, cudaStream_t s);
-// a tensor map of K-major byte rows in 128-byte blocks (api.cu)
-bool encode_blocks(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t parts,
-                   uint64_t part_bytes, uint32_t box_rows);
+// a tensor map of K-major rows in 128-element blocks (api.cu)
+bool encode_blocks(CUtensorMap* tm, const void* base, bool e2m1, uint64_t cols, uint64_t rows, uint64_t row_bytes,
+                   uint32_t parts, uint64_t part_bytes, uint32_t box_rows, uint32_t box_parts);
 
 }  // namespace moe

@@ -26,26 +26,25 @@ namespace {
 
 constexpr int kTileN = 128;      // weight rows of a tile (MMA M)
 constexpr int kMaxRows = 192;    // token rows of a tile (MMA N): two accumulators and the scales fit TMEM
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 12;
 constexpr int kMaxCluster = 8;
+constexpr uint32_t kPairBytes = 16384;
 constexpr int kStep = 2;         // K blocks (of 128) that a weight loader takes at once: 128 bytes of a row
 constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at once: 16 bytes of a row
-// Warps by role. Two warps that take the ring's slots in turn (issuers, rows'
-// copies) need an even number of slots, so that a slot's phases are all seen by
-// one of them: a warp that had missed one could take its parity for the one it
-// waits for.
-constexpr int kIssuer = 4, kCodesW = 6, kCodesX = 7, kCopyX = 9, kLoadW = 11, kWarps = 19;  // (epilogue: 0-3)
-constexpr int kLoaders = kWarps - kLoadW;
+// Warps by role. Two warps that take the ring's slots in turn (issuers, rows)
+// need an even number of slots, so that a slot's phases are all seen by one of
+// them: a warp that had missed one could take its parity for the one it waits for.
+constexpr int kIssuer = 4, kRowsX = 6, kCodesW = 8, kCopyW = 10, kWarps = 16;  // (epilogue: 0-3)
+constexpr int kMaxCopiers = 5;   // warps that copy weights
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kABytes = kTileN * 128;
-constexpr uint32_t kRawBytes = kStep * kTileN * 64;
 constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct LinearParams {
-  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
-  const uint8_t* w;      // [N][K / 2]
+  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]; a box has all of one product, of a pair half of one part
+  CUtensorMap tm_w;      // the weights: [K / 128][N][128 of 4 bits], a box one K block of a tile
   const uint8_t* wc;     // [N][K / 32]
   const uint8_t* xc[2];  // [M][K / 32]
   __nv_bfloat16* out;
@@ -58,11 +57,13 @@ struct LinearParams {
   int stacked;           // two parts as columns of one product (few rows), else as two products
   int cols;              // columns of a product (MMA N): nt, stacked 2 nt
   int slots;             // of the ring: a K block's weights, rows and scale images each
-  int ahead;             // steps that a weight loader has under way (1, 2 or 4)
+  int copiers;           // warps that copy weights in turn (a divisor of `slots`)
+  int code_warps;        // warps that make the weights' scale images (1 or 2)
   int issuers;           // 1 or 2, each with its own accumulators
-  int copiers;           // warps that copy rows (1 or 2)
+  int turns;             // one product: warps that take its rows in turn (1 or 2)
   int split;             // CTAs (a cluster) that share a tile's K
-  uint32_t off_b, slot_b, off_img, slot_img, off_raw, off_xchg, off_bar;
+  int pair;              // CTAs (a cluster) with neighbouring tiles of the same rows: each copies half to both
+  uint32_t off_b, slot_b, off_img, slot_img, off_xchg, off_bar;
 };
 
 struct Bars {
@@ -82,17 +83,19 @@ using ptx::mbar_wait_clocks;
 // What a CTA goes through: its cluster's tiles, and of each the same K blocks
 // (its share of K, from an even one on).
 struct Work {
-  int first, step;  // tiles
+  int first, step;  // tiles (of a pair: two at a time)
   int rank;
   int nk, k0, k1;
+  int pair_n;       // the CTA's weight rows behind those of its pair's first tile
 };
 
 __device__ __forceinline__ Work work_of(const LinearParams& p) {
   Work w;
-  const int S = p.split;
-  w.rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
-  w.first = static_cast<int>(blockIdx.x) / S;
-  w.step = static_cast<int>(gridDim.x) / S;
+  const int S = p.split, cluster = p.pair ? 2 : S;
+  w.first = static_cast<int>(blockIdx.x) / cluster;
+  w.step = static_cast<int>(gridDim.x) / cluster;
+  w.rank = p.pair ? 0 : static_cast<int>(blockIdx.x) - w.first * cluster;
+  w.pair_n = p.pair ? (static_cast<int>(blockIdx.x) & 1) * kTileN : 0;
   w.nk = p.K / 128;
   const int steps = (w.nk + kStep - 1) / kStep;
   w.k0 = kStep * (steps * w.rank / S);
@@ -100,7 +103,9 @@ __device__ __forceinline__ Work work_of(const LinearParams& p) {
   return w;
 }
 
-__device__ __forceinline__ int tile_n(const LinearParams& p, int t) { return t / p.tiles_m * kTileN; }
+__device__ __forceinline__ int tile_n(const LinearParams& p, const Work& w, int t) {
+  return (t / p.tiles_m << p.pair) * kTileN + w.pair_n;
+}
 __device__ __forceinline__ int tile_m(const LinearParams& p, int t) { return t % p.tiles_m * p.nt; }
 
 // A place in the ring, and the parity of its present phase.
@@ -115,119 +120,6 @@ struct Slot {
     }
   }
 };
-
-// 16 bytes of weights to shared memory; the 256 bytes around them come to L2 with them.
-__device__ __forceinline__ void copy_weights(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-__device__ __forceinline__ void st_shared_v2(uint32_t at, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
-}
-
-// Weights by one of the loader warps, its 16 rows of every tile: 128 bytes of a
-// row (two K blocks) to 8 lanes, 16 bytes each, `ahead` such steps on their way
-// to a place that only this thread reads again; then into the ring as the
-// tensor cores read E2M1 rows: 16 codes (8 bytes) in a unit of 16 bytes, whose
-// other half is not looked at, the units of a row of 128 permuted by the row
-// (128-byte swizzle).
-__device__ __forceinline__ void load_tiles(const LinearParams& p, const Work& w, Bars* bars, uint32_t sbase, int loader) {
-  const int lane = threadIdx.x & 31, sub = lane >> 3, half = (lane >> 2) & 1, c = lane & 3;
-  volatile int* abort = &bars->abort;
-  const long long pitch = p.K / 2;
-  const int row0 = 16 * loader + sub;
-  const int steps = (w.k1 - w.k0 + kStep - 1) / kStep;
-  const bool odd = (w.k1 - w.k0) & 1;  // the last step of a tile has one K block
-  const int tiles = w.first < p.tasks ? (p.tasks - 1 - w.first) / w.step + 1 : 0;
-  const int total = steps * tiles;
-  // rows 4 i further: the same permutation for i even, and for i odd
-  uint32_t at[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      at[i][u] = sbase + (row0 + 4 * i) * 128 + (((2 * c + u) ^ ((sub + 4 * i) & 7)) << 4);
-  const int ahead = p.ahead;
-  const uint32_t raw = sbase + p.off_raw + (loader * 128 + lane) * 16;  // + 16 KB a step, 512 every fourth row
-  const uint32_t raw_end = raw + ahead * kRawBytes;
-  // the next step to load
-  int lt = w.first, left_l = 0;
-  const uint8_t* src[4];
-  const auto load = [&](uint32_t dst) {
-    if (left_l == 0) {  // a tile's first
-      const int n0 = tile_n(p, lt);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // (rows past the last repeat it)
-        src[i] = p.w + min(n0 + row0 + 4 * i, p.N - 1) * pitch + w.k0 * 64 + (lane & 7) * 16;
-      left_l = steps;
-      lt += w.step;
-    }
-    --left_l;
-    if (half == 0 || left_l > 0 || !odd) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) copy_weights(dst + i * 512, src[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) src[i] += kStep * 64;
-  };
-  for (int j = 0; j < ahead; ++j) {
-    if (j < total) load(raw + j * kRawBytes);
-    copy_commit();
-  }
-  __syncthreads();  // the barriers are there
-  if (p.split > 1) ptx::cluster_arrive();
-  Slot a, b;  // of the step's first and second K block
-  b.next(p.slots);
-  int left = steps;
-  uint32_t from = raw;
-  const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full);
-  for (int i = 0; i < total; ++i) {
-    --left;
-    const bool two = left > 0 || !odd;
-    if (ahead == 4)
-      copy_wait<3>();
-    else if (ahead == 2)
-      copy_wait<1>();
-    else
-      copy_wait<0>();
-    uint4 v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
-                   : "r"(from + q * 512)
-                   : "memory");
-    bool ok = mbar_wait_clocks(empty0 + a.at * 8, a.phase ^ 1, abort);
-    if (two) ok = ok && mbar_wait_clocks(empty0 + b.at * 8, b.phase ^ 1, abort);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    if (half == 0 || two) {
-      const uint32_t to = (half ? b.at : a.at) * kABytes;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        st_shared_v2(to + (q >> 1) * 1024 + at[q & 1][0], v[q].x, v[q].y);
-        st_shared_v2(to + (q >> 1) * 1024 + at[q & 1][1], v[q].z, v[q].w);
-      }
-    }
-    __syncwarp();
-    if (elect_one()) {
-      ptx::mbar_arrive(full0 + a.at * 8);
-      if (two) ptx::mbar_arrive(full0 + b.at * 8);
-    }
-    if (i + ahead < total) load(from);  // (what was there is in the ring)
-    copy_commit();
-    from += kRawBytes;
-    if (from == raw_end) from = raw;
-    if (left == 0) left = steps;
-    a.next(p.slots, two ? 2 : 1);
-    b.next(p.slots, two ? 2 : 1);
-  }
-  copy_wait<0>();
-}
 
 // 4 K blocks' codes of one row (word j: the block 4 g + j), as 16 bytes where a
 // row's codes are 16-byte aligned; the 128 bytes around them come to L2 too.
@@ -253,20 +145,19 @@ struct Codes {
   uint4 v[kImages][4];
 };
 
-template <int kImages, bool kRows>
-__device__ __forceinline__ void load_group(const LinearParams& p, const Work& w, const uint8_t* codes, bool wide,
-                                           int t, int g, Codes<kImages>& c) {
+template <int kImages>
+__device__ __forceinline__ void load_group(const LinearParams& p, const Work& w, int part, bool wide, int t, int g,
+                                           Codes<kImages>& c) {
   const int lane = threadIdx.x & 31;
-  const int r0 = kRows ? tile_m(p, t) : tile_n(p, t);
-  const int rows = min((kRows ? p.M : p.N) - r0, kRows ? p.nt : kTileN);
+  const int r0 = tile_m(p, t), rows = min(p.M - r0, p.nt);
   const long long pitch = p.K / 32;
 #pragma unroll
   for (int i = 0; i < kImages; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       int r = 128 * i + 32 * q + lane;
-      const uint8_t* from = codes;
-      if (kRows && p.stacked && r >= p.nt) {  // lo behind hi
+      const uint8_t* from = p.xc[part];
+      if (p.stacked && r >= p.nt) {  // lo behind hi
         r -= p.nt;
         from = p.xc[1];
       }
@@ -279,45 +170,134 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
-// Scale images by one warp: a K block's codes as tcgen05.cp reads them: lane
-// i's 16 bytes hold the 4 codes each of the rows i, 32 + i, 64 + i, 96 + i.
-// Codes are loaded 4 K blocks at a time, one such group ahead. kRows: of the
-// rows' part `part`, else the weights'.
-template <int kImages, bool kRows>
-__device__ __forceinline__ void scale_images(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int part) {
-  const int lane = threadIdx.x & 31;
+// A K block's scale image as tcgen05.cp reads it: lane i's 16 bytes hold the 4
+// codes each of the rows i, 32 + i, 64 + i, 96 + i.
+__device__ __forceinline__ void store_image(uint8_t* img, const uint4 (&v)[4], int j) {
+  *reinterpret_cast<uint4*>(img) = make_uint4(word(v[0], j), word(v[1], j), word(v[2], j), word(v[3], j));
+}
+
+// The weights' scale images by two warps, groups of 4 K blocks in turn; the
+// next group's codes are on their way meanwhile. (A warp is 5 stages at most
+// behind what it last saw of the ring, which has 6 slots or more or one warp.)
+__device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int turn) {
+  const int lane = threadIdx.x & 31, turns = p.code_warps;
   volatile int* abort = &bars->abort;
-  const uint8_t* codes = kRows ? p.xc[part] : p.wc;
-  const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(codes) & 15) == 0;  // (the workspace's are aligned)
-  uint8_t* base = smem + p.off_img + (kRows ? 1 + part * kImages : 0) * kImg + lane * 16;
-  const int g0 = w.k0 / kGroup;
-  Codes<kImages> next;
-  if (w.first < p.tasks) load_group<kImages, kRows>(p, w, codes, wide, w.first, g0, next);
+  const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.wc) & 15) == 0;
+  const long long pitch = p.K / 32;
+  const int g0 = w.k0 / kGroup, g1 = (w.k1 + kGroup - 1) / kGroup;
+  int t = w.first, g = g0;  // of the group to load next
+  const auto fetch = [&](uint4 (&v)[4]) {
+    const int n0 = tile_n(p, w, t);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = make_uint4(0, 0, 0, 0);
+      const int n = n0 + 32 * q + lane;
+      if (n < p.N) v[q] = load_codes(p.wc + n * pitch, g, w.nk, wide);
+    }
+  };
+  const auto advance = [&](int n) {
+    for (g += n; g >= g1; g -= g1 - g0) t += w.step;
+  };
+  uint4 next[4];
+  advance(turn);
+  if (t < p.tasks) fetch(next);
   __syncthreads();  // the barriers are there
-  if (p.split > 1) ptx::cluster_arrive();
+  if (p.split > 1 || p.pair) ptx::cluster_arrive();
   Slot slot;
+  uint8_t* base = smem + p.off_img + lane * 16;
+  int to_go = turn;
+  for (int u = w.first; u < p.tasks; u += w.step) {
+    for (int k = w.k0; k < w.k1;) {
+      const int end = min(w.k1, (k / kGroup + 1) * kGroup);
+      if (to_go > 0) {  // the other warp's
+        --to_go;
+        slot.next(p.slots, end - k);
+        k = end;
+        continue;
+      }
+      to_go = turns - 1;
+      uint4 now[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) now[q] = next[q];
+      advance(turns);
+      if (t < p.tasks) fetch(next);
+      for (; k < end; ++k, slot.next(p.slots)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)))
+          return;
+        store_image(base + slot.at * p.slot_img, now, k % kGroup);
+        __syncwarp();
+        if (elect_one()) ptx::mbar_arrive(ptx::smem_u32(&bars->full[slot.at]));
+      }
+    }
+  }
+}
+
+// The rows of one product, of the part `part`, by one warp, or by `turns` in
+// turn, this one `turn`: a K block's rows by a tensor copy (of a pair each CTA
+// copies half of them to both), and their scale images. Codes are loaded 4 K
+// blocks at a time, one such group ahead.
+template <int kImages>
+__device__ __forceinline__ void load_rows(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int part,
+                                          int turn, int turns) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = ptx::policy_evict_last();
+  const int parts = p.stacked ? 2 : 1;  // of this product
+  const uint32_t bytes = static_cast<uint32_t>(parts * p.nt) * 128u;
+  const uint32_t rows0 = ptx::smem_u32(smem) + p.off_b + part * bytes;
+  const int half = (blockIdx.x & 1) * (p.nt >> 1);
+  volatile int* abort = &bars->abort;
+  const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.xc[part]) & 15) == 0;  // (the workspace's are aligned)
+  uint8_t* base = smem + p.off_img + (1 + part * kImages) * kImg + lane * 16;
+  const int g0 = w.k0 / kGroup;
+  Codes<kImages> next;  // (of two images' rows only the present group is held)
+  if (kImages == 1 && w.first < p.tasks) load_group<kImages>(p, w, part, wide, w.first, g0, next);
+  __syncthreads();  // the barriers are there
+  if (p.split > 1 || p.pair) ptx::cluster_arrive();
+  Slot slot;
+  int to_go = turn;
   for (int t = w.first; t < p.tasks; t += w.step) {
+    const int row = tile_m(p, t);
     Codes<kImages> now;
     for (int k = w.k0; k < w.k1; ++k) {
       const int j = k % kGroup;
       if (k == w.k0 || j == 0) {
         now = next;
-        if (k - j + kGroup < w.k1)
-          load_group<kImages, kRows>(p, w, codes, wide, t, k / kGroup + 1, next);
+        if (kImages > 1)
+          load_group<kImages>(p, w, part, wide, t, k / kGroup, now);
+        else if (k - j + kGroup < w.k1)
+          load_group<kImages>(p, w, part, wide, t, k / kGroup + 1, next);
         else if (t + w.step < p.tasks)
-          load_group<kImages, kRows>(p, w, codes, wide, t + w.step, g0, next);
+          load_group<kImages>(p, w, part, wide, t + w.step, g0, next);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort))) return;
-      uint8_t* dst = base + slot.at * p.slot_img;
+      if (to_go == 0) {
+        to_go = turns;
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)))
+          return;
+        uint8_t* dst = base + slot.at * p.slot_img;
 #pragma unroll
-      for (int m = 0; m < kImages; ++m)
-        *reinterpret_cast<uint4*>(dst + m * kImg) =
-            make_uint4(word(now.v[m][0], j), word(now.v[m][1], j), word(now.v[m][2], j), word(now.v[m][3], j));
-      __syncwarp();
-      if (elect_one()) ptx::mbar_arrive(ptx::smem_u32(&bars->full[slot.at]));
+        for (int m = 0; m < kImages; ++m) store_image(dst + m * kImg, now.v[m], j);
+        __syncwarp();
+        if (elect_one()) {
+          const uint32_t full = ptx::smem_u32(&bars->full[slot.at]), to = rows0 + slot.at * p.slot_b;
+          ptx::mbar_arrive_expect_tx(full, bytes);
+          if (p.pair) {
+            for (int h = 0; h < parts; ++h)
+              ptx::tma_load_4d_multicast(to + (h * p.nt + half) * 128, &p.tm_x, 0, row + half, part + h, k, full, 3,
+                                         policy);
+          } else {
+            ptx::tma_load_4d(to, &p.tm_x, 0, row, part, k, full, policy);
+          }
+        }
+        __syncwarp();
+      }
+      --to_go;
       slot.next(p.slots);
     }
   }
+  // a pair: the other's signs that it has read the last slots, before this CTA may end
+  if (p.pair)
+    for (int i = 0; i < p.slots; ++i, slot.next(p.slots))
+      if (!mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)) return;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
@@ -332,21 +312,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const Work w = work_of(p);
   const int himg = p.cols > 128 ? 2 : 1;            // scale images of a product's columns
   const int products = p.stacked ? 1 : p.parts;     // of a K block
+  const bool clustered = S > 1 || p.pair;
 
   if (warp == 0) {
     if (lane < kMaxSlots) {
-      ptx::mbar_init(bar(bars->full[lane]), kLoaders + 1 + 1 + products);  // weights, rows, images of both
-      ptx::mbar_init(bar(bars->empty[lane]), 1);
-    } else if (lane < 10) {
-      ptx::mbar_init(bar(bars->tfull[lane - 8]), p.issuers);
-      ptx::mbar_init(bar(bars->tempty[lane - 8]), 4);
-    } else if (lane == 10) {
+      ptx::mbar_init(bar(bars->full[lane]), 2 + products);  // weights, their images, each product's rows
+      ptx::mbar_init(bar(bars->empty[lane]), 1 + p.pair);
+    } else if (lane >= 16 && lane < 18) {
+      ptx::mbar_init(bar(bars->tfull[lane - 16]), p.issuers);
+      ptx::mbar_init(bar(bars->tempty[lane - 16]), 4);
+    } else if (lane == 18) {
       ptx::mbar_init(bar(bars->efree), S);
-    } else if (lane == 11) {
+    } else if (lane == 19) {
       ptx::mbar_init(bar(bars->efull), 4 * S);
-    } else if (lane == 12) {
+    } else if (lane == 20) {
       ptx::mbar_init(bar(bars->drain), p.issuers);
-    } else if (lane == 13) {
+    } else if (lane == 21) {
       bars->abort = 0;
     }
     ptx::fence_mbar_init();
@@ -354,39 +335,52 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem), kTmemCols);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
-  } else if (warp == kCopyX && elect_one()) {
+  } else if (warp == kRowsX && elect_one()) {
     ptx::prefetch_tmap(&p.tm_x);
+  } else if (warp >= kCopyW && warp < kCopyW + p.copiers && elect_one()) {
+    // The first blocks' weights on their way to L2 (which takes nothing that
+    // the kernel before may still change) while the barriers are made.
+    for (int k = w.k0 + warp - kCopyW; k < min(w.k1, w.k0 + p.slots) && w.first < p.tasks; k += p.copiers)
+      ptx::prefetch_tensor_3d(&p.tm_w, 0, tile_n(p, w, w.first), k);
   }
   __syncwarp();
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   // (every branch waits for the barriers' initialisation, and in a cluster says
   // that its CTA's are there)
-  if (warp >= kLoadW) {
-    load_tiles(p, w, bars, sbase, warp - kLoadW);
-  } else if (warp == kCodesW) {
-    scale_images<1, false>(p, w, bars, smem, 0);
-  } else if (warp >= kCodesX && warp < kCodesX + products) {
+  if (warp >= kCodesW && warp < kCodesW + p.code_warps) {
+    weight_codes(p, w, bars, smem, warp - kCodesW);
+  } else if (warp >= kRowsX && warp < kRowsX + max(products, p.turns)) {
+    const int who = warp - kRowsX, part = products > 1 ? who : 0;
+    const int turn = products > 1 ? 0 : who, turns = products > 1 ? 1 : p.turns;
     if (himg == 1)
-      scale_images<1, true>(p, w, bars, smem, warp - kCodesX);
+      load_rows<1>(p, w, bars, smem, part, turn, turns);
     else
-      scale_images<2, true>(p, w, bars, smem, warp - kCodesX);
+      load_rows<2>(p, w, bars, smem, part, turn, turns);
   } else {
     __syncthreads();
-    if (S > 1) ptx::cluster_arrive();
+    if (clustered) {
+      ptx::cluster_arrive();
+      ptx::cluster_wait();  // the others' barriers
+    }
     ptx::tc_fence_after();
   }
+  const bool waits = (warp >= kCodesW && warp < kCodesW + p.code_warps) || (warp >= kRowsX && warp < kRowsX + max(products, p.turns));
 
-  if (warp >= kCopyX && warp < kCopyX + p.copiers) {
-    // ------------------------------------------------------------ rows' copies
+  if (warp >= kCopyW && warp < kCopyW + p.copiers) {
+    // ------------------------------------------------------------ weights
+    // A 4-bit box spreads its codes as the tensor cores read E2M1 rows: 16 (8
+    // bytes) in a unit of 16 bytes, whose other half is not looked at. A thread
+    // that issues tensor copies gets one through in some 400 ns, so several
+    // warps take the slots in turn.
     if (elect_one()) {
-      const uint64_t policy = ptx::policy_evict_last();
-      const int me = warp - kCopyX;
+      const uint64_t policy = p.tiles_m > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+      const int me = warp - kCopyW;
       int turn = 0;
       Slot slot;
       bool ok = true;
       for (int t = w.first; ok && t < p.tasks; t += w.step) {
-        const int row = tile_m(p, t);
+        const int n0 = tile_n(p, w, t);
         for (int k = w.k0; k < w.k1; ++k, slot.next(p.slots)) {
           const bool mine = turn == me;
           if (++turn == p.copiers) turn = 0;
@@ -396,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             break;
           }
           const uint32_t full = bar(bars->full[slot.at]);
-          ptx::mbar_arrive_expect_tx(full, p.slot_b);
-          ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, row, 0, k, full, policy);
+          ptx::mbar_arrive_expect_tx(full, kABytes / 2);  // (a 4-bit box counts its global bytes)
+          ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, k, full, policy);
         }
       }
     }
@@ -449,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
               some = 1;
             }
           }
-          ptx::tc_commit(bar(bars->empty[slot.at]));
+          if (p.pair)
+            ptx::tc_commit_multicast(bar(bars->empty[slot.at]), 3);
+          else
+            ptx::tc_commit(bar(bars->empty[slot.at]));
         }
         if (ok) ptx::tc_commit(bar(bars->tfull[acc]));
         acc ^= 1;
@@ -481,9 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const uint32_t xchg = sbase + p.off_xchg + tid * 16;
     int lt = 0;
     bool ok = true;
-    if (S > 1) ptx::cluster_wait();  // (every warp arrived; the others wait at the end)
     for (int t = w.first; t < p.tasks; t += w.step, ++lt) {
-      const int n = tile_n(p, t) + tid, m0 = tile_m(p, t);
+      const int n = tile_n(p, w, t) + tid, m0 = tile_m(p, t);
       const int cols = min(p.nt, p.M - m0);
       const int acc = lt & 1;
       ok = ok && __all_sync(0xffffffffu, mbar_wait_clocks(bar(bars->tfull[acc]), (lt >> 1) & 1, abort));
@@ -573,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   }
 
   // ------------------------------------------------------------ teardown
-  if (S > 1 && warp >= kIssuer) ptx::cluster_wait();
+  if (clustered && waits) ptx::cluster_wait();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort && tid == 0) {
@@ -589,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     ptx::tc_fence_after();
     ptx::tmem_dealloc(bars->tmem, kTmemCols);
   }
-  if (S > 1) {  // nobody writes here any more
+  if (clustered) {  // nobody writes here any more
     ptx::cluster_arrive();
     ptx::cluster_wait();
   }
@@ -700,7 +696,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   if (K < 128 || K % 128 || K > (1 << 16)) return MOE_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MOE_OK;
   if (!x || !w || !w_codes || !out) return MOE_ERR_ARG;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(w_codes, 4) || !aligned(out, 2) || !aligned(x_codes, 4) ||
+  if (!aligned(x, 16) || !aligned(w, 32) || !aligned(w_codes, 4) || !aligned(out, 2) || !aligned(x_codes, 4) ||
       !aligned(status, 4) || !aligned(workspace, 16) || ldx % (x_codes ? 16 : 8))
     return MOE_ERR_ALIGN;
   if (ldx < K || ldo < N) return MOE_ERR_ARG;
@@ -714,7 +710,6 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   LinearParams p = {};
-  p.w = w;
   p.wc = w_codes;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
@@ -756,22 +751,29 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
       clusters = c;
     }
   }
+  // Tiles whose rows' bytes outweigh the weights': two CTAs share them.
+  const int tiles_n = (N + kTileN - 1) / kTileN, pairs = max_clusters(device, 2);
+  if (split == 1 && p.slot_b >= kPairBytes && tiles_n > 1 && pairs > 0) {
+    p.pair = 1;
+    p.tasks = (tiles_n + 1) / 2 * p.tiles_m;
+    clusters = pairs;
+  }
   p.split = split;
-  clusters = static_cast<int>(std::min<int64_t>(clusters, tasks));
+  clusters = std::min(clusters, p.tasks);
   const uint32_t xchg = split > 1 ? static_cast<uint32_t>((p.nt / 4 + split - 1) / split * split) * 2048u : 0;
-  const bool over = tasks <= clusters;  // the exchange buffer lies over the rings
-  // few rows wait for the weights from HBM, more for the tensor cores
-  p.ahead = p.cols <= 128 ? 4 : p.slot_b <= 32768 ? 2 : 1;
-  const uint32_t room = fixed - (over ? 0 : xchg) - p.ahead * kRawBytes;
-  p.slots = static_cast<int>(std::min<uint32_t>(room / (kABytes + p.slot_b + p.slot_img), kMaxSlots));
-  if (p.slots > 4 || p.issuers > 1) p.slots &= ~1;
-  p.copiers = p.slots % 2 == 0 ? 2 : 1;
+  const bool over = p.tasks <= clusters;  // the exchange buffer lies over the rings
+  const uint32_t room = fixed - (over ? 0 : xchg);
+  const uint32_t by_tmem = (kTmemCols - 2 * p.issuers * p.cols) / (4 + 4 * products * himg);
+  p.slots = static_cast<int>(std::min<uint32_t>({room / (kABytes + p.slot_b + p.slot_img), by_tmem, kMaxSlots}));
+  if (p.slots > 3 || p.issuers > 1) p.slots &= ~1;
+  p.copiers = p.slots % 5 == 0 ? 5 : p.slots % 4 == 0 ? 4 : p.slots % 3 == 0 ? 3 : p.slots;
+  p.code_warps = p.slots >= 6 ? 2 : 1;
+  p.turns = p.slots % 2 == 0 ? 2 : 1;
   if (p.slots < 2) return MOE_ERR_UNSUPPORTED;  // (no size reaches this)
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
-  p.off_raw = p.off_img + p.slots * p.slot_img;
-  p.off_xchg = over ? 0 : p.off_raw + p.ahead * kRawBytes;
-  p.off_bar = p.off_raw + p.ahead * kRawBytes + (over ? 0 : xchg);
+  p.off_xchg = over ? 0 : p.off_img + p.slots * p.slot_img;
+  p.off_bar = p.off_img + p.slots * p.slot_img + (over ? 0 : xchg);
   if (over && xchg > p.off_img) return MOE_ERR_UNSUPPORTED;
 
   const uint8_t* rows = static_cast<const uint8_t*>(x);
@@ -797,10 +799,14 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
       return MOE_ERR_CUDA;
     }
   }
-  if (!encode_blocks(&p.tm_x, rows, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K, p.nt)) return MOE_ERR_CUDA;
+  if (!encode_blocks(&p.tm_w, w, true, K, N, K / 2, 0, 0, kTileN, 1)) return MOE_ERR_CUDA;
+  if (!encode_blocks(&p.tm_x, rows, false, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K,
+                     p.pair ? p.nt / 2 : p.nt, p.stacked && !p.pair ? 2 : 1))
+    return MOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+  const unsigned cluster = p.pair ? 2 : split;
+  cfg.gridDim = dim3(clusters * cluster);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemMax;
   cfg.stream = st;
@@ -808,9 +814,9 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  attr[1].val.clusterDim = {cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();

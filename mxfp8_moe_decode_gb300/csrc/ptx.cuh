@@ -222,6 +222,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int3
       : "memory");
 }
 
+// The same to the CTAs of the cluster in `mask`, each completing on its own
+// mbarrier at the same place.
+__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                      int32_t w, uint32_t bar, uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7, %8;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "h"(mask), "l"(policy)
+      : "memory");
+}
+
 // Contiguous bulk copy global -> shared (size and both addresses multiples of 16).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -295,6 +306,14 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
                : "memory");
+}
+
+// The same, arriving on the mbarrier at that place in each CTA of the cluster in `mask`.
+__device__ __forceinline__ void tc_commit_multicast(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
 }
 
 // Shared -> TMEM copy of a 32-row x 128-bit matrix, replicated into all four
