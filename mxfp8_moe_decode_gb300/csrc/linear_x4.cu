@@ -35,7 +35,7 @@ constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at onc
 // need an even number of slots, so that a slot's phases are all seen by one of
 // them: a warp that had missed one could take its parity for the one it waits for.
 constexpr int kIssuer = 4, kRowsX = 6, kCodesW = 8, kCopyW = 10, kWarps = 16;  // (epilogue: 0-3)
-constexpr int kMaxCopiers = 5;   // warps that copy weights
+static_assert(kWarps - kCopyW >= 5, "warps that copy weights");
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kABytes = kTileN * 128;
 constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
@@ -110,9 +110,8 @@ __device__ __forceinline__ int tile_m(const LinearParams& p, int t) { return t %
 
 // A place in the ring, and the parity of its present phase.
 struct Slot {
-  int at = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int n, int by = 1) {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n, uint32_t by) {
     at += by;
     if (at >= n) {
       at -= n;
@@ -205,30 +204,32 @@ __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& 
   if (p.split > 1 || p.pair) ptx::cluster_arrive();
   Slot slot;
   uint8_t* base = smem + p.off_img + lane * 16;
-  int to_go = turn;
+  const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full), R = p.slots;
+  int at = turn;  // of this warp's next group in the present tile
   for (int u = w.first; u < p.tasks; u += w.step) {
-    for (int k = w.k0; k < w.k1;) {
-      const int end = min(w.k1, (k / kGroup + 1) * kGroup);
-      if (to_go > 0) {  // the other warp's
-        --to_go;
-        slot.next(p.slots, end - k);
-        k = end;
-        continue;
-      }
-      to_go = turns - 1;
+    int k = w.k0;
+    for (; at < g1 - g0; at += turns) {
+      const int begin = max(w.k0, (g0 + at) * kGroup), end = min(w.k1, (g0 + at + 1) * kGroup);
+      if (begin > k) slot.next(R, begin - k);  // (at most a group's: the other warp's)
       uint4 now[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) now[q] = next[q];
       advance(turns);
       if (t < p.tasks) fetch(next);
-      for (; k < end; ++k, slot.next(p.slots)) {
-        if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)))
-          return;
-        store_image(base + slot.at * p.slot_img, now, k % kGroup);
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int kj = (g0 + at) * kGroup + j;
+        if (kj < begin || kj >= end) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort))) return;
+        store_image(base + slot.at * p.slot_img, now, j);
         __syncwarp();
-        if (elect_one()) ptx::mbar_arrive(ptx::smem_u32(&bars->full[slot.at]));
+        if (elect_one()) ptx::mbar_arrive(full0 + slot.at * 8);
+        slot.next(R, 1);
       }
+      k = end;
     }
+    if (w.k1 > k) slot.next(R, w.k1 - k);
+    at -= g1 - g0;
   }
 }
 
@@ -254,50 +255,51 @@ __device__ __forceinline__ void load_rows(const LinearParams& p, const Work& w, 
   __syncthreads();  // the barriers are there
   if (p.split > 1 || p.pair) ptx::cluster_arrive();
   Slot slot;
-  int to_go = turn;
+  slot.at = turn;
+  const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full), R = p.slots;
+  int k = w.k0 + turn;  // this warp's next block in the present tile
+  int next_t = w.first, next_g = g0;
   for (int t = w.first; t < p.tasks; t += w.step) {
     const int row = tile_m(p, t);
     Codes<kImages> now;
-    for (int k = w.k0; k < w.k1; ++k) {
-      const int j = k % kGroup;
-      if (k == w.k0 || j == 0) {
-        now = next;
-        if (kImages > 1)
-          load_group<kImages>(p, w, part, wide, t, k / kGroup, now);
-        else if (k - j + kGroup < w.k1)
-          load_group<kImages>(p, w, part, wide, t, k / kGroup + 1, next);
-        else if (t + w.step < p.tasks)
-          load_group<kImages>(p, w, part, wide, t + w.step, g0, next);
-      }
-      if (to_go == 0) {
-        to_go = turns;
-        if (!__all_sync(0xffffffffu, mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)))
-          return;
-        uint8_t* dst = base + slot.at * p.slot_img;
-#pragma unroll
-        for (int m = 0; m < kImages; ++m) store_image(dst + m * kImg, now.v[m], j);
-        __syncwarp();
-        if (elect_one()) {
-          const uint32_t full = ptx::smem_u32(&bars->full[slot.at]), to = rows0 + slot.at * p.slot_b;
-          ptx::mbar_arrive_expect_tx(full, bytes);
-          if (p.pair) {
-            for (int h = 0; h < parts; ++h)
-              ptx::tma_load_4d_multicast(to + (h * p.nt + half) * 128, &p.tm_x, 0, row + half, part + h, k, full, 3,
-                                         policy);
-          } else {
-            ptx::tma_load_4d(to, &p.tm_x, 0, row, part, k, full, policy);
-          }
+    for (int have = -1; k < w.k1; k += turns, slot.next(R, turns)) {
+      if (k / kGroup != have) {
+        have = k / kGroup;
+        if (kImages == 1 && next_t == t && next_g == have)
+          now = next;
+        else  // (not guessed: the other warp had all the blocks in between)
+          load_group<kImages>(p, w, part, wide, t, have, now);
+        if (kImages == 1) {
+          next_t = (have + 1) * kGroup < w.k1 ? t : t + w.step;
+          next_g = next_t == t ? have + 1 : g0;
+          if (next_t < p.tasks) load_group<kImages>(p, w, part, wide, next_t, next_g, next);
         }
-        __syncwarp();
       }
-      --to_go;
-      slot.next(p.slots);
+      const int j = k % kGroup;
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort))) return;
+      uint8_t* dst = base + slot.at * p.slot_img;
+#pragma unroll
+      for (int m = 0; m < kImages; ++m) store_image(dst + m * kImg, now.v[m], j);
+      __syncwarp();
+      if (elect_one()) {
+        const uint32_t full = full0 + slot.at * 8, to = rows0 + slot.at * p.slot_b;
+        ptx::mbar_arrive_expect_tx(full, bytes);
+        if (p.pair) {
+          for (int h = 0; h < parts; ++h)
+            ptx::tma_load_4d_multicast(to + (h * p.nt + half) * 128, &p.tm_x, 0, row + half, part + h, k, full, 3,
+                                       policy);
+        } else {
+          ptx::tma_load_4d(to, &p.tm_x, 0, row, part, k, full, policy);
+        }
+      }
+      __syncwarp();
     }
+    k += w.k0 - w.k1;
   }
-  // a pair: the other's signs that it has read the last slots, before this CTA may end
+  // a pair: the other's signs that it has read this warp's last slots, before the CTA may end
   if (p.pair)
-    for (int i = 0; i < p.slots; ++i, slot.next(p.slots))
-      if (!mbar_wait_clocks(ptx::smem_u32(&bars->empty[slot.at]), slot.phase ^ 1, abort)) return;
+    for (int i = 0; i < p.slots; i += turns, slot.next(R, turns))
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort))) return;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
@@ -376,23 +378,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     if (elect_one()) {
       const uint64_t policy = p.tiles_m > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
       const int me = warp - kCopyW;
-      int turn = 0;
+      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots, turns = p.copiers;
       Slot slot;
+      slot.at = me;
+      int k = w.k0 + me;  // this warp's next block in the present tile
       bool ok = true;
       for (int t = w.first; ok && t < p.tasks; t += w.step) {
         const int n0 = tile_n(p, w, t);
-        for (int k = w.k0; k < w.k1; ++k, slot.next(p.slots)) {
-          const bool mine = turn == me;
-          if (++turn == p.copiers) turn = 0;
-          if (!mine) continue;
-          if (!mbar_wait_clocks(bar(bars->empty[slot.at]), slot.phase ^ 1, abort)) {
+        for (; k < w.k1; k += turns, slot.next(R, turns)) {
+          if (!mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort)) {
             ok = false;
             break;
           }
-          const uint32_t full = bar(bars->full[slot.at]);
+          const uint32_t full = full0 + slot.at * 8;
           ptx::mbar_arrive_expect_tx(full, kABytes / 2);  // (a 4-bit box counts its global bytes)
           ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, k, full, policy);
         }
+        k += w.k0 - w.k1;
       }
     }
     __syncwarp();
@@ -405,52 +407,54 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       // is a multiple of 4 only.)
       const uint32_t sfx = 4 * himg, sf_slot = 4 + products * sfx;
       const uint32_t sf0 = tmem + 2 * p.issuers * p.cols;
-      const uint32_t part_bytes = static_cast<uint32_t>(p.nt) * 128u;
+      const uint32_t part_units = static_cast<uint32_t>(p.nt) * 8u;  // of 16 bytes, as descriptors count
       const uint32_t idesc = ptx::idesc_mxf8(p.cols, 0, ptx::kFmtE2M1), idesc_k = ptx::idesc_mxf8(0, 1, 0) - ptx::idesc_mxf8(0, 0, 0);
-      uint32_t turn = 0, acc = 0, acc_phase = 1;
+      const uint64_t a0 = ptx::sdesc_k128_sw128(sbase), b0 = ptx::sdesc_k128_sw128(sbase + p.off_b),
+                     i0 = ptx::sdesc_rows16(sbase + p.off_img);
+      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots, turns = p.issuers;
+      const uint32_t slot_b = p.slot_b >> 4, slot_img = p.slot_img >> 4;
+      uint32_t acc = 0, acc_phase = 1;
       Slot slot;
+      slot.at = me;
+      int k = w.k0 + static_cast<int>(me);  // this issuer's next block in the present tile
       bool ok = true;
       for (int t = w.first; ok && t < p.tasks; t += w.step) {
         if (!mbar_wait_clocks(bar(bars->tempty[acc]), acc_phase, abort)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + (acc * p.issuers + me) * p.cols;
         uint32_t some = 0;
-        for (int k = w.k0; k < w.k1; ++k, slot.next(p.slots)) {
-          const bool mine = turn == me;
-          if (++turn == static_cast<uint32_t>(p.issuers)) turn = 0;
-          if (!mine) continue;
-          if (!mbar_wait_clocks(bar(bars->full[slot.at]), slot.phase, abort)) {
+        for (; k < w.k1; k += turns, slot.next(R, turns)) {
+          if (!mbar_wait_clocks(full0 + slot.at * 8, slot.phase, abort)) {
             ok = false;
             break;
           }
-          // The weights and images that other warps wrote, to the tensor cores'
-          // view of shared memory.
+          // The images that other warps wrote, to the tensor cores' view of
+          // shared memory.
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
-          const uint32_t a = sbase + slot.at * kABytes;
-          const uint32_t b = sbase + p.off_b + slot.at * p.slot_b;
-          const uint32_t img = sbase + p.off_img + slot.at * p.slot_img;
+          const uint64_t a = a0 + slot.at * (kABytes >> 4), img = i0 + slot.at * slot_img;
+          uint64_t b = b0 + slot.at * slot_b;
           const uint32_t sfa = sf0 + slot.at * sf_slot;
-          ptx::tc_cp_32x128b_x4(sfa, ptx::sdesc_rows16(img));
-          for (int h = 0; h < products; ++h) {
+          ptx::tc_cp_32x128b_x4(sfa, img);
+          for (int h = 0; h < products; ++h, b += part_units) {
             const uint32_t sx = sfa + 4 + h * sfx;
             for (int i = 0; i < himg; ++i)
-              ptx::tc_cp_32x128b_x4(sx + 4 * i, ptx::sdesc_rows16(img + (1 + h * himg + i) * kImg));
+              ptx::tc_cp_32x128b_x4(sx + 4 * i, img + (1 + h * himg + i) * (kImg >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              ptx::tc_mma_mxf8(d, ptx::sdesc_k128_sw128(a + 32 * kk), ptx::sdesc_k128_sw128(b + h * part_bytes + 32 * kk),
-                               idesc + kk * idesc_k, sfa, sx, some);
+              ptx::tc_mma_mxf8(d, a + 2 * kk, b + 2 * kk, idesc + kk * idesc_k, sfa, sx, some);
               some = 1;
             }
           }
           if (p.pair)
-            ptx::tc_commit_multicast(bar(bars->empty[slot.at]), 3);
+            ptx::tc_commit_multicast(empty0 + slot.at * 8, 3);
           else
-            ptx::tc_commit(bar(bars->empty[slot.at]));
+            ptx::tc_commit(empty0 + slot.at * 8);
         }
         if (ok) ptx::tc_commit(bar(bars->tfull[acc]));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
+        k += w.k0 - w.k1;
       }
       // everything this thread issued has completed once drain fires
       ptx::tc_commit(bar(bars->drain));
