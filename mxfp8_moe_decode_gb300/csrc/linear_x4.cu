@@ -28,7 +28,6 @@ constexpr int kTileN = 128;      // weight rows of a tile (MMA M)
 constexpr int kMaxRows = 192;    // token rows of a tile (MMA N): two accumulators and the scales fit TMEM
 constexpr int kMaxSlots = 12;
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kPairBytes = 16384;
 constexpr int kStep = 2;         // K blocks (of 128) that a weight loader takes at once: 128 bytes of a row
 constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at once: 16 bytes of a row
 // Warps by role. Two warps that take the ring's slots in turn (issuers, rows)
@@ -43,7 +42,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct LinearParams {
-  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]; a box has all of one product, of a pair half of one part
+  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
   CUtensorMap tm_w;      // the weights: [K / 128][N][128 of 4 bits], a box one K block of a tile
   const uint8_t* wc;     // [N][K / 32]
   const uint8_t* xc[2];  // [M][K / 32]
@@ -51,7 +50,7 @@ struct LinearParams {
   long long ldo;
   int* status;
   int M, N, K;
-  int nt;                // token rows of a tile (a multiple of 16)
+  int nt;                // token rows of a tile (a multiple of 16, stacked of 8)
   int tiles_m, tasks;
   int parts;             // 1 (MXFP8 rows) or 2 (bf16 rows as hi and lo)
   int stacked;           // two parts as columns of one product (few rows), else as two products
@@ -62,7 +61,6 @@ struct LinearParams {
   int issuers;           // 1 or 2, each with its own accumulators
   int turns;             // one product: warps that take its rows in turn (1 or 2)
   int split;             // CTAs (a cluster) that share a tile's K
-  int pair;              // CTAs (a cluster) with neighbouring tiles of the same rows: each copies half to both
   uint32_t off_b, slot_b, off_img, slot_img, off_xchg, off_bar;
 };
 
@@ -83,19 +81,17 @@ using ptx::mbar_wait_clocks;
 // What a CTA goes through: its cluster's tiles, and of each the same K blocks
 // (its share of K, from an even one on).
 struct Work {
-  int first, step;  // tiles (of a pair: two at a time)
+  int first, step;  // tiles
   int rank;
   int nk, k0, k1;
-  int pair_n;       // the CTA's weight rows behind those of its pair's first tile
 };
 
 __device__ __forceinline__ Work work_of(const LinearParams& p) {
   Work w;
-  const int S = p.split, cluster = p.pair ? 2 : S;
-  w.first = static_cast<int>(blockIdx.x) / cluster;
-  w.step = static_cast<int>(gridDim.x) / cluster;
-  w.rank = p.pair ? 0 : static_cast<int>(blockIdx.x) - w.first * cluster;
-  w.pair_n = p.pair ? (static_cast<int>(blockIdx.x) & 1) * kTileN : 0;
+  const int S = p.split;
+  w.first = static_cast<int>(blockIdx.x) / S;
+  w.step = static_cast<int>(gridDim.x) / S;
+  w.rank = static_cast<int>(blockIdx.x) - w.first * S;
   w.nk = p.K / 128;
   const int steps = (w.nk + kStep - 1) / kStep;
   w.k0 = kStep * (steps * w.rank / S);
@@ -103,9 +99,7 @@ __device__ __forceinline__ Work work_of(const LinearParams& p) {
   return w;
 }
 
-__device__ __forceinline__ int tile_n(const LinearParams& p, const Work& w, int t) {
-  return (t / p.tiles_m << p.pair) * kTileN + w.pair_n;
-}
+__device__ __forceinline__ int tile_n(const LinearParams& p, int t) { return t / p.tiles_m * kTileN; }
 __device__ __forceinline__ int tile_m(const LinearParams& p, int t) { return t % p.tiles_m * p.nt; }
 
 // A place in the ring, and the parity of its present phase.
@@ -186,7 +180,7 @@ __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& 
   const int g0 = w.k0 / kGroup, g1 = (w.k1 + kGroup - 1) / kGroup;
   int t = w.first, g = g0;  // of the group to load next
   const auto fetch = [&](uint4 (&v)[4]) {
-    const int n0 = tile_n(p, w, t);
+    const int n0 = tile_n(p, t);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       v[q] = make_uint4(0, 0, 0, 0);
@@ -200,8 +194,6 @@ __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& 
   uint4 next[4];
   advance(turn);
   if (t < p.tasks) fetch(next);
-  __syncthreads();  // the barriers are there
-  if (p.split > 1 || p.pair) ptx::cluster_arrive();
   Slot slot;
   uint8_t* base = smem + p.off_img + lane * 16;
   const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full), R = p.slots;
@@ -233,34 +225,25 @@ __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& 
   }
 }
 
-// The rows of one product, of the part `part`, by one warp, or by `turns` in
-// turn, this one `turn`: a K block's rows by a tensor copy (of a pair each CTA
-// copies half of them to both), and their scale images. Codes are loaded 4 K
-// blocks at a time, one such group ahead.
+// The scale images of a product's rows, of the part `part`, by one warp, or by
+// `turns` in turn, this one `turn`. Codes are loaded 4 K blocks at a time, one
+// such group ahead.
 template <int kImages>
-__device__ __forceinline__ void load_rows(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int part,
+__device__ __forceinline__ void row_codes(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int part,
                                           int turn, int turns) {
   const int lane = threadIdx.x & 31;
-  const uint64_t policy = ptx::policy_evict_last();
-  const int parts = p.stacked ? 2 : 1;  // of this product
-  const uint32_t bytes = static_cast<uint32_t>(parts * p.nt) * 128u;
-  const uint32_t rows0 = ptx::smem_u32(smem) + p.off_b + part * bytes;
-  const int half = (blockIdx.x & 1) * (p.nt >> 1);
   volatile int* abort = &bars->abort;
   const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.xc[part]) & 15) == 0;  // (the workspace's are aligned)
   uint8_t* base = smem + p.off_img + (1 + part * kImages) * kImg + lane * 16;
   const int g0 = w.k0 / kGroup;
   Codes<kImages> next;  // (of two images' rows only the present group is held)
   if (kImages == 1 && w.first < p.tasks) load_group<kImages>(p, w, part, wide, w.first, g0, next);
-  __syncthreads();  // the barriers are there
-  if (p.split > 1 || p.pair) ptx::cluster_arrive();
   Slot slot;
   slot.at = turn;
   const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full), R = p.slots;
   int k = w.k0 + turn;  // this warp's next block in the present tile
   int next_t = w.first, next_g = g0;
   for (int t = w.first; t < p.tasks; t += w.step) {
-    const int row = tile_m(p, t);
     Codes<kImages> now;
     for (int have = -1; k < w.k1; k += turns, slot.next(R, turns)) {
       if (k / kGroup != have) {
@@ -281,25 +264,10 @@ __device__ __forceinline__ void load_rows(const LinearParams& p, const Work& w, 
 #pragma unroll
       for (int m = 0; m < kImages; ++m) store_image(dst + m * kImg, now.v[m], j);
       __syncwarp();
-      if (elect_one()) {
-        const uint32_t full = full0 + slot.at * 8, to = rows0 + slot.at * p.slot_b;
-        ptx::mbar_arrive_expect_tx(full, bytes);
-        if (p.pair) {
-          for (int h = 0; h < parts; ++h)
-            ptx::tma_load_4d_multicast(to + (h * p.nt + half) * 128, &p.tm_x, 0, row + half, part + h, k, full, 3,
-                                       policy);
-        } else {
-          ptx::tma_load_4d(to, &p.tm_x, 0, row, part, k, full, policy);
-        }
-      }
-      __syncwarp();
+      if (elect_one()) ptx::mbar_arrive(full0 + slot.at * 8);
     }
     k += w.k0 - w.k1;
   }
-  // a pair: the other's signs that it has read this warp's last slots, before the CTA may end
-  if (p.pair)
-    for (int i = 0; i < p.slots; i += turns, slot.next(R, turns))
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort))) return;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
@@ -314,19 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const Work w = work_of(p);
   const int himg = p.cols > 128 ? 2 : 1;            // scale images of a product's columns
   const int products = p.stacked ? 1 : p.parts;     // of a K block
-  const bool clustered = S > 1 || p.pair;
 
   if (warp == 0) {
     if (lane < kMaxSlots) {
-      ptx::mbar_init(bar(bars->full[lane]), 2 + products);  // weights, their images, each product's rows
-      ptx::mbar_init(bar(bars->empty[lane]), 1 + p.pair);
+      ptx::mbar_init(bar(bars->full[lane]), 2 + products);  // the copies, the weights' images, each product's rows'
+      ptx::mbar_init(bar(bars->empty[lane]), 1);
     } else if (lane >= 16 && lane < 18) {
       ptx::mbar_init(bar(bars->tfull[lane - 16]), p.issuers);
       ptx::mbar_init(bar(bars->tempty[lane - 16]), 4);
     } else if (lane == 18) {
       ptx::mbar_init(bar(bars->efree), S);
     } else if (lane == 19) {
-      ptx::mbar_init(bar(bars->efull), 4 * S);
+      ptx::mbar_init(bar(bars->efull), 1);
     } else if (lane == 20) {
       ptx::mbar_init(bar(bars->drain), p.issuers);
     } else if (lane == 21) {
@@ -337,45 +304,40 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem), kTmemCols);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
-  } else if (warp == kRowsX && elect_one()) {
-    ptx::prefetch_tmap(&p.tm_x);
   } else if (warp >= kCopyW && warp < kCopyW + p.copiers && elect_one()) {
     // The first blocks' weights on their way to L2 (which takes nothing that
     // the kernel before may still change) while the barriers are made.
+    ptx::prefetch_tmap(&p.tm_x);
     for (int k = w.k0 + warp - kCopyW; k < min(w.k1, w.k0 + p.slots) && w.first < p.tasks; k += p.copiers)
-      ptx::prefetch_tensor_3d(&p.tm_w, 0, tile_n(p, w, w.first), k);
+      ptx::prefetch_tensor_3d(&p.tm_w, 0, tile_n(p, w.first), k);
   }
   __syncwarp();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (S > 1) {  // the others' barriers are there
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  // (every branch waits for the barriers' initialisation, and in a cluster says
-  // that its CTA's are there)
+
   if (warp >= kCodesW && warp < kCodesW + p.code_warps) {
     weight_codes(p, w, bars, smem, warp - kCodesW);
   } else if (warp >= kRowsX && warp < kRowsX + max(products, p.turns)) {
     const int who = warp - kRowsX, part = products > 1 ? who : 0;
     const int turn = products > 1 ? 0 : who, turns = products > 1 ? 1 : p.turns;
     if (himg == 1)
-      load_rows<1>(p, w, bars, smem, part, turn, turns);
+      row_codes<1>(p, w, bars, smem, part, turn, turns);
     else
-      load_rows<2>(p, w, bars, smem, part, turn, turns);
-  } else {
-    __syncthreads();
-    if (clustered) {
-      ptx::cluster_arrive();
-      ptx::cluster_wait();  // the others' barriers
-    }
-    ptx::tc_fence_after();
-  }
-  const bool waits = (warp >= kCodesW && warp < kCodesW + p.code_warps) || (warp >= kRowsX && warp < kRowsX + max(products, p.turns));
-
-  if (warp >= kCopyW && warp < kCopyW + p.copiers) {
-    // ------------------------------------------------------------ weights
+      row_codes<2>(p, w, bars, smem, part, turn, turns);
+  } else if (warp >= kCopyW && warp < kCopyW + p.copiers) {
+    // ------------------------------------------------------------ copies
     // A 4-bit box spreads its codes as the tensor cores read E2M1 rows: 16 (8
     // bytes) in a unit of 16 bytes, whose other half is not looked at. A thread
     // that issues tensor copies gets one through in some 400 ns, so several
     // warps take the slots in turn.
     if (elect_one()) {
+      const uint64_t keep = ptx::policy_evict_last();
       const uint64_t policy = p.tiles_m > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
       const int me = warp - kCopyW;
       const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots, turns = p.copiers;
@@ -384,15 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       int k = w.k0 + me;  // this warp's next block in the present tile
       bool ok = true;
       for (int t = w.first; ok && t < p.tasks; t += w.step) {
-        const int n0 = tile_n(p, w, t);
+        const int n0 = tile_n(p, t), m0 = tile_m(p, t);
         for (; k < w.k1; k += turns, slot.next(R, turns)) {
           if (!mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort)) {
             ok = false;
             break;
           }
           const uint32_t full = full0 + slot.at * 8;
-          ptx::mbar_arrive_expect_tx(full, kABytes / 2);  // (a 4-bit box counts its global bytes)
+          ptx::mbar_arrive_expect_tx(full, kABytes / 2 + p.slot_b);  // (a 4-bit box counts its global bytes)
           ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, k, full, policy);
+          ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, m0, 0, k, full, keep);
         }
         k += w.k0 - w.k1;
       }
@@ -446,10 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
               some = 1;
             }
           }
-          if (p.pair)
-            ptx::tc_commit_multicast(empty0 + slot.at * 8, 3);
-          else
-            ptx::tc_commit(empty0 + slot.at * 8);
+          ptx::tc_commit(empty0 + slot.at * 8);
         }
         if (ok) ptx::tc_commit(bar(bars->tfull[acc]));
         acc ^= 1;
@@ -480,10 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const uint32_t lanes = bars->tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const int per = (p.nt / 4 + S - 1) / S;  // groups of 4 columns that a CTA of the cluster sums
     const uint32_t xchg = sbase + p.off_xchg + tid * 16;
+    const bool over = p.off_xchg == 0;
     int lt = 0;
     bool ok = true;
     for (int t = w.first; t < p.tasks; t += w.step, ++lt) {
-      const int n = tile_n(p, w, t) + tid, m0 = tile_m(p, t);
+      const int n = tile_n(p, t) + tid, m0 = tile_m(p, t);
       const int cols = min(p.nt, p.M - m0);
       const int acc = lt & 1;
       ok = ok && __all_sync(0xffffffffu, mbar_wait_clocks(bar(bars->tfull[acc]), (lt >> 1) & 1, abort));
@@ -521,13 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         if (lane == 0) ptx::mbar_arrive(bar(bars->tempty[acc]));
         continue;
       }
-      // Columns 4 c .. 4 c + 3 of the tile are summed by the CTA c % S. Every CTA
-      // says that its buffer is free (its last tile's sums are read; where the
-      // buffer lies over the ring, all MMAs are done too), sends its parts of
-      // the columns to their CTAs, and adds up those it gets in the order of the ranks.
-      if (tid < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), tid));
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efree), lt & 1, abort));
-      if (!ok) continue;
+      // Columns 4 c .. 4 c + 3 of the tile are summed by the CTA c % S: every CTA
+      // sends its parts of the columns to their CTAs, and adds up those it gets
+      // in the order of the ranks. Where a buffer lies over the ring, or still
+      // holds the last tile's parts, its CTA first says that it is free (all
+      // MMAs are done, the sums are read).
+      if (over || lt > 0) {
+        if (tid < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), tid));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efree), (over ? 0 : lt - 1) & 1, abort));
+        if (!ok) continue;
+      }
+      const int groups = (cols + 3) / 4, own = groups > w.rank ? (groups - w.rank + S - 1) / S : 0;
+      if (tid == 0) ptx::mbar_arrive_expect_tx(bar(bars->efull), static_cast<uint32_t>(own * S) * 2048u);
       int owner = 0;
       uint32_t at = xchg + w.rank * per * 2048;
       for (int c0 = 0; c0 < cols; c0 += 16) {
@@ -536,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           if (c0 + j < cols) {
-            ptx::st_cluster_v4(ptx::cluster_addr(at, owner), v[j], v[j + 1], v[j + 2], v[j + 3]);
+            ptx::st_async_v4(ptx::cluster_addr(at, owner), v[j], v[j + 1], v[j + 2], v[j + 3],
+                             ptx::cluster_addr(bar(bars->efull), owner));
             if (++owner == S) {
               owner = 0;
               at += 2048;
@@ -545,10 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
       }
       ptx::tc_fence_before();
-      ptx::fence_cluster();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars->tempty[acc]));
-      if (lane < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efull), lane));
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efull), lt & 1, abort));
       if (!ok) continue;
       if (n < p.N) {
@@ -573,26 +538,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   }
 
   // ------------------------------------------------------------ teardown
-  if (clustered && waits) ptx::cluster_wait();
+  // In a cluster nobody ends before all others have sent what they send.
+  if (S > 1) ptx::cluster_arrive();
   ptx::tc_fence_before();
   __syncthreads();
-  if (*abort && tid == 0) {
-    if (p.status) atomicOr(p.status, MOE_LINEAR_STATUS_TIMEOUT);
-    // copies still under way land before the shared memory goes (in a run
-    // without errors all of them are consumed)
-    const long long t0 = clock64();
-    while (clock64() - t0 < ptx::kWaitClocks / 100) {
+  if (*abort) {
+    if (tid == 0) {
+      if (p.status) atomicOr(p.status, MOE_LINEAR_STATUS_TIMEOUT);
+      // copies still under way land before the shared memory goes (in a run
+      // without errors all of them are consumed)
+      const long long t0 = clock64();
+      while (clock64() - t0 < ptx::kWaitClocks / 100) {
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp == kIssuer) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(bars->tmem, kTmemCols);
   }
-  if (clustered) {  // nobody writes here any more
-    ptx::cluster_arrive();
-    ptx::cluster_wait();
-  }
+  if (S > 1) ptx::cluster_wait();
 }
 
 // ---------------------------------------------------------------- bf16 rows as two MXFP8 rows
@@ -653,7 +618,7 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams p) {
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
 
-int round16(int v) { return (v + 15) / 16 * 16; }
+int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // How many clusters of each size the device holds at once (looked up once per device).
 int max_clusters(int device, int split) {
@@ -723,7 +688,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.K = K;
   p.parts = x_codes ? 1 : 2;
   p.tiles_m = (M + kMaxRows - 1) / kMaxRows;
-  p.nt = round16((M + p.tiles_m - 1) / p.tiles_m);
+  p.nt = round_up((M + p.tiles_m - 1) / p.tiles_m, 16);
   const int64_t tasks = static_cast<int64_t>((N + kTileN - 1) / kTileN) * p.tiles_m;
   if (tasks > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
   p.tasks = static_cast<int>(tasks);
@@ -731,6 +696,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   // rows' two parts are columns of one product; the products of more are two
   // that share their scales' copies and weights.
   p.stacked = p.parts == 2 && p.nt <= 64;
+  if (p.stacked) p.nt = round_up(M, 8);
   p.cols = p.stacked ? 2 * p.nt : p.nt;
   p.issuers = p.cols <= 96 ? 2 : 1;  // (their accumulators fit TMEM; the time of wider products hides the issue)
   const int himg = p.cols > 128 ? 2 : 1, products = p.stacked ? 1 : p.parts;
@@ -755,17 +721,10 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
       clusters = c;
     }
   }
-  // Tiles whose rows' bytes outweigh the weights': two CTAs share them.
-  const int tiles_n = (N + kTileN - 1) / kTileN, pairs = max_clusters(device, 2);
-  if (split == 1 && p.slot_b >= kPairBytes && tiles_n > 1 && pairs > 0) {
-    p.pair = 1;
-    p.tasks = (tiles_n + 1) / 2 * p.tiles_m;
-    clusters = pairs;
-  }
   p.split = split;
   clusters = std::min(clusters, p.tasks);
   const uint32_t xchg = split > 1 ? static_cast<uint32_t>((p.nt / 4 + split - 1) / split * split) * 2048u : 0;
-  const bool over = p.tasks <= clusters;  // the exchange buffer lies over the rings
+  const bool over = split > 1 && p.nt > 64;  // the exchange buffer lies over the ring (one tile a cluster)
   const uint32_t room = fixed - (over ? 0 : xchg);
   const uint32_t by_tmem = (kTmemCols - 2 * p.issuers * p.cols) / (4 + 4 * products * himg);
   p.slots = static_cast<int>(std::min<uint32_t>({room / (kABytes + p.slot_b + p.slot_img), by_tmem, kMaxSlots}));
@@ -805,12 +764,11 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   }
   if (!encode_blocks(&p.tm_w, w, true, K, N, K / 2, 0, 0, kTileN, 1)) return MOE_ERR_CUDA;
   if (!encode_blocks(&p.tm_x, rows, false, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K,
-                     p.pair ? p.nt / 2 : p.nt, p.stacked && !p.pair ? 2 : 1))
+                     p.nt, p.parts))
     return MOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
-  const unsigned cluster = p.pair ? 2 : split;
-  cfg.gridDim = dim3(clusters * cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemMax;
   cfg.stream = st;
@@ -818,9 +776,9 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {cluster, 1, 1};
+  attr[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
