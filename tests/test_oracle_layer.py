@@ -1,0 +1,87 @@
+"""Hand-worked pins of oracle.layer, and of the frequencies a program makes for
+the rotary positions (CPU)."""
+
+import math
+
+import numpy as np
+import pytest
+
+from mxfp8_moe_decode_gb300 import rope_freqs
+from oracle import layer as L
+
+
+def test_block_residual():
+    x, r = np.array([[3.0, 4.0]]), np.array([[1.0, -1.0]])
+    # rms = sqrt((9 + 16) / 2) = 5 / sqrt 2
+    res, b = L.block_residual(x, r, np.array([2.0, 1.0]), np.array([0.5, 3.0]), 0.5, 2.0, eps=0.0)
+    want = 2.0 * np.array([[0.5 * 2.0 * 3.0, 3.0 * 4.0]]) * math.sqrt(2) / 5
+    assert np.allclose(b, want, rtol=1e-15) and np.allclose(res, 0.5 * r + want, rtol=1e-15)
+    res, b = L.block_residual(x, r)
+    assert np.array_equal(b, x) and np.array_equal(res, x + r)
+
+
+def test_turns_are_whole_numbers():
+    assert L.turns(3, 1 << 62) == 0.75
+    assert L.turns(5, 1 << 62) == 0.25
+    assert L.turns(-1, 1 << 62) == 0.75
+    assert L.turns((1 << 31) - 1, (1 << 33) + 1) == (((1 << 31) - 1) * ((1 << 33) + 1) % (1 << 64)) / 2.0 ** 64
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_by_quarter_turns(interleaved):
+    x = np.arange(1.0, 9.0).reshape(1, 1, 8)
+    # pair 0 by a quarter turn, pair 1 by a half turn; the last four dims stay
+    out = L.rope(x, [1], [1 << 62, 1 << 63], 0, interleaved, 2.0)[0, 0]
+    u, v = ([0, 2], [1, 3]) if interleaved else ([0, 1], [2, 3])
+    want = x[0, 0].copy()
+    want[u[0]], want[v[0]] = -2 * x[0, 0, v[0]], 2 * x[0, 0, u[0]]
+    want[u[1]], want[v[1]] = -2 * x[0, 0, u[1]], -2 * x[0, 0, v[1]]
+    assert np.allclose(out, want, atol=1e-14)
+
+
+def test_linear_by_hand():
+    # one row of 32 columns: 1.5 at column 0, -6 at column 1, 0.5 at column 31, scale 2
+    w = np.zeros((1, 16), np.uint8)
+    w[0, 0], w[0, 15] = 0x3 | (0xF << 4), 0x1 << 4
+    x = np.zeros((1, 32))
+    x[0, 0], x[0, 1], x[0, 31] = 1.0, 10.0, 4.0
+    out, size = L.linear(x, w, np.array([[128]], np.uint8))
+    assert out[0, 0] == 2 * (1.5 - 60.0 + 2.0) and size[0, 0] == 2 * (1.5 + 60.0 + 2.0)
+
+
+def unsigned(t):
+    return [int(v) % (1 << 64) for v in t.tolist()]
+
+
+def test_rope_freqs():
+    f = unsigned(rope_freqs(8, base=16.0, device="cpu"))
+    want = [16.0 ** (-i / 4) / (2 * math.pi) * 2.0 ** 64 for i in range(4)]
+    assert all(abs(a - b) <= 2.0 ** -52 * b for a, b in zip(f, want))
+    slow = unsigned(rope_freqs(8, base=16.0, factor=4.0, device="cpu"))  # (whole numbers again)
+    assert all(abs(a - b / 4) <= 1 for a, b in zip(slow, f))
+    # radians beyond half a turn wrap; the given ones are taken as they are
+    assert unsigned(rope_freqs(4, inv_freq=[math.pi, 1.5 * math.pi], device="cpu")) == [1 << 63, 3 << 62]
+
+
+def test_rope_freqs_by_parts():
+    """Fast pairs keep their frequency, slow ones are divided, between them a line."""
+    plain = unsigned(rope_freqs(64, base=10000.0, device="cpu"))
+    got = unsigned(rope_freqs(64, base=10000.0, factor=8.0, trained=4096, device="cpu"))
+
+    def pair(turns):
+        return 32 * math.log(4096 / (turns * 2 * math.pi)) / math.log(10000.0)
+
+    low, high = math.floor(pair(32.0)), math.ceil(pair(1.0))
+    assert 0 < low < high < 32
+    for i in range(32):
+        mix = min(max((i - low) / (high - low), 0.0), 1.0)
+        want = plain[i] * (1 - mix + mix / 8.0)
+        # (both are rounded to whole numbers: half of one each)
+        assert abs(got[i] - want) <= 2.0 ** -50 * want + 1
+
+
+@pytest.mark.parametrize("kw", [dict(rot=0), dict(rot=7), dict(rot=8, factor=0.0), dict(rot=8, factor=float("nan")),
+                                dict(rot=8, inv_freq=[1.0]), dict(rot=4, inv_freq=[1.0, float("inf")])])
+def test_rope_freqs_refusals(kw):
+    with pytest.raises(ValueError):
+        rope_freqs(device="cpu", **kw)
