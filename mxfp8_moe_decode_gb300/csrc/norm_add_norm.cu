@@ -24,6 +24,35 @@ namespace {
 
 constexpr int kThreads = kSeamOwners;
 
+// Two fp32 values in one 64-bit register: one instruction for both, each
+// rounded as by itself.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ Pair pair(uint32_t bf16x2) {
+  return pair(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 floats(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+  return f;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
 struct NormAddNormParams {
   const __nv_bfloat16* x;
   const __nv_bfloat16* residual;
@@ -65,88 +94,94 @@ __global__ void __launch_bounds__(kThreads) norm_add_norm_kernel(const NormAddNo
     s[i] = in ? __ldcs(rr + o) : zero;
     g[i] = in && gated ? (p.ldg ? __ldcs(gr + o) : __ldg(gr + o)) : zero;
   }
-  float rx = 1.0f;
+  float rx = p.block_scale;
   if (post) {
-    float ss = 0.0f;
+    Pair q0 = pair(0.0f, 0.0f), q1 = q0;
 #pragma unroll
-    for (int i = 0; i < kOct; ++i) {
-      if (tid + i * kThreads < noct) {
-        float v[8];
-        unpack_bf16x8(b[i], v);
-        ss = seam_sumsq_octet(v, ss);
-      }
+    for (int i = 0; i < kOct; ++i) {  // (octets past the row are zeros)
+      const Pair a = pair(b[i].x), c = pair(b[i].y), d = pair(b[i].z), e = pair(b[i].w);
+      q0 = fma(d, d, fma(a, a, q0));
+      q1 = fma(e, e, fma(c, c, q1));
     }
-    ss = seam_warp_sum(ss);
+    const float2 u = floats(q0), v = floats(q1);
+    const float ss = seam_warp_sum((u.x + u.y) + (v.x + v.y));
     if ((tid & 31) == 0) red[0][tid >> 5] = ss;
     __syncthreads();
-    rx = seam_scale(red[0], H, p.eps);
+    const float tot = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+    rx *= __frsqrt_rn(tot / static_cast<float>(H) + p.eps);
   }
+  // block_scale * rx, one factor
+  const Pair f = pair(rx, rx), rs = pair(p.res_scale, p.res_scale);
   float ss = 0.0f;
   uint4* ro = reinterpret_cast<uint4*>(p.res_out + t * H);
 #pragma unroll
   for (int i = 0; i < kOct; ++i) {
     const int o = tid + i * kThreads;
     if (o < noct) {
-      float x[8], r[8], m[8];
-      unpack_bf16x8(b[i], x);
-      unpack_bf16x8(s[i], r);
-      if (post) {
-        unpack_bf16x8(__ldg(pr + o), m);
+      const uint4 m = post ? __ldg(pr + o) : zero;
+      const uint32_t xs[4] = {b[i].x, b[i].y, b[i].z, b[i].w}, ms[4] = {m.x, m.y, m.z, m.w},
+                     gs[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+      uint32_t r[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (x[j] * rx) * m[j];
+      for (int j = 0; j < 4; ++j) {
+        Pair v = mul(pair(xs[j]), f);
+        if (post) v = mul(v, pair(ms[j]));
+        if (gated) v = mul(v, pair(gs[j]));
+        const float2 n = floats(fma(rs, pair(r[j]), v));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(n.x, n.y);
+        r[j] = *reinterpret_cast<const uint32_t*>(&h);
+        const float2 k = floats(pair(r[j]));  // (the seam's order)
+        ss = fmaf(k.x, k.x, ss);
+        ss = fmaf(k.y, k.y, ss);
       }
-      if (gated) {
-        unpack_bf16x8(g[i], m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= m[j];
-      }
-      __align__(16) __nv_bfloat162 q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[j] = __floats2bfloat162_rn(fmaf(p.res_scale, r[2 * j], p.block_scale * x[2 * j]),
-                                     fmaf(p.res_scale, r[2 * j + 1], p.block_scale * x[2 * j + 1]));
-      s[i] = *reinterpret_cast<const uint4*>(q);
+      s[i] = make_uint4(r[0], r[1], r[2], r[3]);
       ro[o] = s[i];
-      unpack_bf16x8(s[i], r);
-      ss = seam_sumsq_octet(r, ss);
     }
   }
   ss = seam_warp_sum(ss);
   if ((tid & 31) == 0) red[1][tid >> 5] = ss;
   __syncthreads();
   const float r = seam_scale(red[1], H, p.eps);
+  const Pair r2 = pair(r, r);
 
 #pragma unroll
   for (int i = 0; i < kOct; ++i) {
     const int o = tid + i * kThreads;
     if (i * kThreads >= noct) break;  // uniform across the CTA
     const bool in = o < noct;
-    float v[8], w[8], y[8];
-    unpack_bf16x8(in ? s[i] : zero, v);
-    unpack_bf16x8(in ? __ldg(wr + o) : zero, w);
+    const uint4 w = in ? __ldg(wr + o) : zero;
+    const uint32_t vs[4] = {s[i].x, s[i].y, s[i].z, s[i].w}, ws[4] = {w.x, w.y, w.z, w.w};
+    Pair y[4];
     float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[j] = (v[j] * r) * w[j];
-      amax = fmaxf(amax, fabsf(y[j]));
+    for (int j = 0; j < 4; ++j) {
+      y[j] = mul(mul(pair(vs[j]), r2), pair(ws[j]));
+      const float2 u = floats(y[j]);
+      amax = fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y)));
     }
     // the 32-group's amax over its four lanes
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int code = mx_code(amax);
-    const float mul = mx_mul(code);
+    const float up = mx_mul(code);
+    const Pair mm = pair(up, up);
     if (in) {
-      uint2 q;
-      q.x = static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[0] * mul), clamp_e4m3(y[1] * mul))) |
-            (static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[2] * mul), clamp_e4m3(y[3] * mul))) << 16);
-      q.y = static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[4] * mul), clamp_e4m3(y[5] * mul))) |
-            (static_cast<uint32_t>(e4m3x2(clamp_e4m3(y[6] * mul), clamp_e4m3(y[7] * mul))) << 16);
-      reinterpret_cast<uint2*>(p.x8 + t * H)[o] = q;
+      // (the conversion saturates; finite values are at most 448 here)
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = floats(mul(y[j], mm));
+        q[j] = e4m3x2(u.x, u.y);
+      }
+      reinterpret_cast<uint2*>(p.x8 + t * H)[o] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       if ((o & 3) == 0) p.x8c[t * (H >> 5) + (o >> 2)] = static_cast<uint8_t>(code);
       if (p.normed) {
         __align__(16) __nv_bfloat162 n[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = floats(y[j]);
+          n[j] = __floats2bfloat162_rn(u.x, u.y);
+        }
         reinterpret_cast<uint4*>(p.normed + t * H)[o] = *reinterpret_cast<const uint4*>(n);
       }
     }
