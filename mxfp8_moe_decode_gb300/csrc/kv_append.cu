@@ -27,7 +27,8 @@
 // and round it to bf16 before anything looks at it, so the cache gets the bytes
 // it would get from keys that another kernel had turned. A chunk's partner (the
 // other halves of its pairs) is a neighbour lane's chunk. Further CTAs of the
-// same grid, behind these, turn the queries: one launch for q, k and v.
+// same grid turn the queries, spread evenly among these: one launch for q, k and
+// v, and the queries' stream fills the waits of the append's chains.
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"
@@ -105,11 +106,15 @@ struct RopeAppendParams : KvAppendParams {
   __nv_bfloat16* q_out;
   long long ldq, ldqo;      // elements between tokens
   int q_heads, q_groups;    // threads (times D / 16) that share a token's heads
-  unsigned slots, ctas;     // page slots, CTAs of the append (the queries' are behind them)
+  unsigned slots;           // page slots
+  unsigned q_share;         // the queries' part of the CTAs, in units of 2^-32, rounded up
 };
 
 // The chunks that this thread loaded, turned (v[i]: token tid / kRowChunks + i *
-// kThreads / kRowChunks of the CTA's).
+// kThreads / kRowChunks of the CTA's). One chunk's code, gone through in a loop
+// that moves the chunks on by one: unrolled over all of them it was 36 KB, and
+// took 52 us where this takes 42 (two prompts of 4100 tokens, 40 query heads of 128;
+// 6, 7 or 8 CTAs an SM by fewer registers: 42, 43, 46).
 template <int D, int kMax>
 __device__ __forceinline__ void turn_keys(const RopeAppendParams& p, uint4 (&v)[kMax], int count, int first_row,
                                           int first_pos) {
@@ -118,35 +123,52 @@ __device__ __forceinline__ void turn_keys(const RopeAppendParams& p, uint4 (&v)[
   const int chunks = p.spec.rot >> 3, half = chunks >> 1;
   const int at = tid % kRowChunks - (p.spec.first >> 3);  // among the rotated chunks
   const bool turns = at >= 0 && at < chunks, low = at < half;
-  // its pairs: 4 of neighbours, or 8 with the chunk `half` further or back
-  const int pair0 = p.spec.interleaved ? 4 * at : 8 * (low ? at : at - half);
+  // Its pairs: 4 of neighbours, or 8 with the chunk `half` further or back. Of
+  // those 8 each of the two makes the sines and cosines of 4.
+  const int pair0 = p.spec.interleaved ? 4 * at : low ? 8 * at : 8 * (at - half) + 4;
   const int partner = !turns || p.spec.interleaved ? lane : low ? lane + half : lane - half;
-  uint64_t f[8];
+  uint64_t f[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = turns && (j < 4 || !p.spec.interleaved) ? __ldg(p.spec.freqs + pair0 + j) : 0;
-#pragma unroll
-  for (int i = 0; i < kMax; ++i) {
-    if ((tid & ~31) + i * kThreads >= count * kRowChunks) break;  // (uniform in the warp)
+  for (int j = 0; j < 4; ++j) f[j] = turns ? __ldg(p.spec.freqs + pair0 + j) : 0;
+  const auto from = [partner](unsigned long long x) { return __shfl_sync(0xffffffffu, x, partner); };
+  const auto turn_one = [&](uint4& x, int i) {
     const int row = min((tid + i * kThreads) / kRowChunks, count - 1);
     const int pos = p.positions ? __ldg(p.positions + first_row + row) : first_pos + row;
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, v[i].x, partner);
-    o.y = __shfl_sync(0xffffffffu, v[i].y, partner);
-    o.z = __shfl_sync(0xffffffffu, v[i].z, partner);
-    o.w = __shfl_sync(0xffffffffu, v[i].w, partner);
-    if (!turns) continue;
-    float c[8], s[8];
+    Pair c[2], s[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rope::turn(pos, f[j], p.spec.scale, c[j], s[j]);
+    for (int j = 0; j < 2; ++j) rope::turn(pos, f[2 * j], f[2 * j + 1], p.spec.scale, c[j], s[j]);
     if (p.spec.interleaved) {
-      rope::turn_neighbours(v[i], c, s);
-    } else {
-#pragma unroll
-      for (int j = 4; j < 8; ++j) rope::turn(pos, f[j], p.spec.scale, c[j], s[j]);
-      uint4 a = low ? v[i] : o, b = low ? o : v[i];
-      rope::turn_halves(a, b, c, s);
-      v[i] = low ? a : b;
+      if (turns) rope::turn_neighbours(x, c, s);
+      return;
     }
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, x.x, partner);
+    o.y = __shfl_sync(0xffffffffu, x.y, partner);
+    o.z = __shfl_sync(0xffffffffu, x.z, partner);
+    o.w = __shfl_sync(0xffffffffu, x.w, partner);
+    Pair oc[2], os[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      oc[j].v = from(c[j].v);
+      os[j].v = from(s[j].v);
+    }
+    const Pair ac[4] = {low ? c[0] : oc[0], low ? c[1] : oc[1], low ? oc[0] : c[0], low ? oc[1] : c[1]};
+    const Pair as[4] = {low ? s[0] : os[0], low ? s[1] : os[1], low ? os[0] : s[0], low ? os[1] : s[1]};
+    uint4 a = low ? x : o, b = low ? o : x;
+    rope::turn_halves(a, b, ac, as);
+    if (turns) x = low ? a : b;
+  };
+  if (count * kRowChunks <= kThreads) {  // (a decode step's)
+    turn_one(v[0], 0);
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < kMax; ++i) {
+    uint4 x = v[0];
+    if ((tid & ~31) + i * kThreads < count * kRowChunks) turn_one(x, i);  // (uniform in the warp)
+#pragma unroll
+    for (int j = 0; j + 1 < kMax; ++j) v[j] = v[j + 1];
+    v[kMax - 1] = x;
   }
 }
 
@@ -213,13 +235,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Params p) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   int slot_index, head, kv;
-  if constexpr (kRope) {  // one row of CTAs in the same order
-    if (blockIdx.x >= p.ctas) {
-      turn_queries<D>(p, blockIdx.x - p.ctas);
+  if constexpr (kRope) {
+    // One row of CTAs, the queries' spread evenly among the append's: CTA b is
+    // the queries' where b q_share passes a whole number.
+    const unsigned q = __umulhi(blockIdx.x, p.q_share);
+    if (__umulhi(blockIdx.x + 1, p.q_share) != q) {
+      turn_queries<D>(p, q);
       return;
     }
-    slot_index = blockIdx.x % p.slots;
-    const int rest = blockIdx.x / p.slots;
+    const unsigned mine = blockIdx.x - q;
+    slot_index = mine % p.slots;
+    const int rest = mine / p.slots;
     head = rest % p.kv_heads;
     kv = 1 - rest / p.kv_heads;
   } else {
@@ -499,6 +525,7 @@ extern "C" int moe_rope_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seq
   const int64_t q_ctas =
       (static_cast<int64_t>(p.tokens) * p.q_groups * (cache->head_dim / 16) + kThreads - 1) / kThreads;
   if (ctas + q_ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  p.ctas = static_cast<unsigned>(ctas);
+  // (ceil(q 2^32 / all): all times it passes q, not q + 1, whole numbers, as all < 2^32; q < all)
+  p.q_share = static_cast<unsigned>(((static_cast<uint64_t>(q_ctas) << 32) + (ctas + q_ctas) - 1) / (ctas + q_ctas));
   return launch_append(p, cache->head_dim, dim3(static_cast<unsigned>(ctas + q_ctas)), stream);
 }

@@ -15,6 +15,7 @@
 // the octets i, i + 128, ... of the row as packed bf16 (4 registers an octet)
 // from the loads, all issued before the first use, to the stores: a row is read
 // once, and the two sums cost two exchanges of four floats.
+#include "f32x2.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
 #include "seam.cuh"
@@ -23,35 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = kSeamOwners;
-
-// Two fp32 values in one 64-bit register: one instruction for both, each
-// rounded as by itself.
-struct Pair {
-  unsigned long long v;
-};
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
-  return p;
-}
-__device__ __forceinline__ Pair pair(uint32_t bf16x2) {
-  return pair(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xFFFF0000u));
-}
-__device__ __forceinline__ float2 floats(Pair p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
-  return f;
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-  Pair p;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-  return p;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-  Pair p;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return p;
-}
 
 struct NormAddNormParams {
   const __nv_bfloat16* x;
@@ -70,7 +42,7 @@ struct NormAddNormParams {
 
 // kOct octets a thread (H <= 1024 kOct)
 template <int kOct>
-__global__ void __launch_bounds__(kThreads) norm_add_norm_kernel(const NormAddNormParams p) {
+__global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm_add_norm_kernel(const NormAddNormParams p) {
   const size_t t = blockIdx.x;
   const int H = p.H;
   const int noct = H >> 3;

@@ -15,6 +15,8 @@
 
 #include <cstdint>
 
+#include "f32x2.cuh"
+
 namespace moe {
 namespace rope {
 
@@ -27,61 +29,66 @@ struct Spec {
   float scale;
 };
 
-// cos and sin (times scale) of pos * f turns.
-__device__ __forceinline__ void turn(int pos, uint64_t f, float scale, float& c, float& s) {
-  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * f + 0x80000000ull;
-  const uint32_t phase = static_cast<uint32_t>(a >> 32);
-  const uint32_t quarter = (phase + 0x20000000u) >> 30;
-  const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter << 30))) * 0x1.921fb6p-30f;  // 2 pi 2^-32
-  const float z = x * x;
-  float sn = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
-  sn = fmaf(z, sn, 1.0f / 120.0f);
-  sn = fmaf(z, sn, -1.0f / 6.0f);
-  sn = fmaf(z * x, sn, x);
-  float cs = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
-  cs = fmaf(z, cs, 1.0f / 24.0f);
-  cs = fmaf(z, cs, -0.5f);
-  cs = fmaf(z, cs, 1.0f);
-  sn *= scale;
-  cs *= scale;
+// cos and sin (times scale) of pos * f0 and pos * f1 turns.
+__device__ __forceinline__ void turn(int pos, uint64_t f0, uint64_t f1, float scale, Pair& c, Pair& s) {
+  const auto phase = [pos](uint64_t f) {
+    return static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos)) * f + 0x80000000ull) >> 32);
+  };
+  const uint32_t a0 = phase(f0), a1 = phase(f1);
+  const uint32_t q0 = (a0 + 0x20000000u) >> 30, q1 = (a1 + 0x20000000u) >> 30;  // the nearest quarters
+  const auto number = [](float v) { return pair(v, v); };
+  const Pair x = mul(pair(static_cast<float>(static_cast<int32_t>(a0 - (q0 << 30))),
+                          static_cast<float>(static_cast<int32_t>(a1 - (q1 << 30)))),
+                     number(0x1.921fb6p-30f));  // 2 pi 2^-32
+  const Pair z = mul(x, x);
+  Pair sn = fma(z, number(1.0f / 362880.0f), number(-1.0f / 5040.0f));
+  sn = fma(z, sn, number(1.0f / 120.0f));
+  sn = fma(z, sn, number(-1.0f / 6.0f));
+  sn = mul(fma(mul(z, x), sn, x), number(scale));
+  Pair cs = fma(z, number(1.0f / 40320.0f), number(-1.0f / 720.0f));
+  cs = fma(z, cs, number(1.0f / 24.0f));
+  cs = fma(z, cs, number(-0.5f));
+  cs = mul(fma(z, cs, number(1.0f)), number(scale));
   // a quarter turn: (cos, sin) -> (-sin, cos)
-  const float u = quarter & 1 ? sn : cs, v = quarter & 1 ? cs : sn;
-  c = __uint_as_float(__float_as_uint(u) ^ ((quarter + 1) & 2 ? 0x80000000u : 0u));
-  s = __uint_as_float(__float_as_uint(v) ^ (quarter & 2 ? 0x80000000u : 0u));
+  const float2 u = floats(cs), v = floats(sn);
+  const auto sign = [](float w, uint32_t flip) { return __uint_as_float(__float_as_uint(w) ^ (flip << 31)); };
+  c = pair(sign(q0 & 1 ? v.x : u.x, (q0 + 1) >> 1), sign(q1 & 1 ? v.y : u.y, (q1 + 1) >> 1));
+  s = pair(sign(q0 & 1 ? u.x : v.x, q0 >> 1), sign(q1 & 1 ? u.y : v.y, q1 >> 1));
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t rounded(Pair a) {
+  const float2 f = floats(a);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The first or the second of each pair (u, v), turned. (One order of operations
-// wherever a pair is turned, so every kernel gives the same bits.)
-__device__ __forceinline__ float first_of(float u, float v, float c, float s) { return fmaf(u, c, -(v * s)); }
-__device__ __forceinline__ float second_of(float u, float v, float c, float s) { return fmaf(v, c, u * s); }
+// Pairs (u, v), turned: u cos - v sin and v cos + u sin. (One order of
+// operations wherever a pair is turned, so every kernel gives the same bits.)
+__device__ __forceinline__ Pair first_of(Pair u, Pair v, Pair c, Pair s) { return fma(u, c, mul(v, negated(s))); }
+__device__ __forceinline__ Pair second_of(Pair u, Pair v, Pair c, Pair s) { return fma(v, c, mul(u, s)); }
 
 // 8 pairs whose first values are in a, second ones in b.
-__device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const float* c, const float* s) {
+__device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const Pair* c, const Pair* s) {
   uint32_t* x = reinterpret_cast<uint32_t*>(&a);
   uint32_t* y = reinterpret_cast<uint32_t*>(&b);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float u0 = bf16_lo(x[j]), u1 = bf16_hi(x[j]), v0 = bf16_lo(y[j]), v1 = bf16_hi(y[j]);
-    x[j] = pack(first_of(u0, v0, c[2 * j], s[2 * j]), first_of(u1, v1, c[2 * j + 1], s[2 * j + 1]));
-    y[j] = pack(second_of(u0, v0, c[2 * j], s[2 * j]), second_of(u1, v1, c[2 * j + 1], s[2 * j + 1]));
+    const Pair u = pair(x[j]), v = pair(y[j]);
+    x[j] = rounded(first_of(u, v, c[j], s[j]));
+    y[j] = rounded(second_of(u, v, c[j], s[j]));
   }
 }
 
 // 4 pairs of neighbours.
-__device__ __forceinline__ void turn_neighbours(uint4& a, const float* c, const float* s) {
+__device__ __forceinline__ void turn_neighbours(uint4& a, const Pair* c, const Pair* s) {
   uint32_t* x = reinterpret_cast<uint32_t*>(&a);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float u = bf16_lo(x[j]), v = bf16_hi(x[j]);
-    x[j] = pack(first_of(u, v, c[j], s[j]), second_of(u, v, c[j], s[j]));
+  for (int j = 0; j < 2; ++j) {
+    const float2 p = floats(pair(x[2 * j])), q = floats(pair(x[2 * j + 1]));
+    const Pair u = pair(p.x, q.x), v = pair(p.y, q.y);
+    const float2 m = floats(first_of(u, v, c[j], s[j])), n = floats(second_of(u, v, c[j], s[j]));
+    x[2 * j] = rounded(pair(m.x, n.x));
+    x[2 * j + 1] = rounded(pair(m.y, n.y));
   }
 }
 
@@ -112,7 +119,7 @@ __device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int po
   int c0, c1;
   const bool turns = item_chunks(r, j, c0, c1);
   constexpr int kAhead = 4;  // heads whose loads are under way together
-  float c[kPairs], s[kPairs];
+  Pair c[kPairs / 2], s[kPairs / 2];
   bool have = false;
   for (int h = h0; h < t.heads; h += kAhead * step) {
     uint4 a[kAhead], b[kAhead];
@@ -128,8 +135,7 @@ __device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int po
 #pragma unroll
       for (int i = 0; i < kPairs; i += 2) {
         const ulonglong2 f = __ldg(reinterpret_cast<const ulonglong2*>(r.freqs + kPairs * j + i));
-        turn(pos, f.x, r.scale, c[i], s[i]);
-        turn(pos, f.y, r.scale, c[i + 1], s[i + 1]);
+        turn(pos, f.x, f.y, r.scale, c[i / 2], s[i / 2]);
       }
       have = true;
     }
@@ -140,7 +146,7 @@ __device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int po
       if (turns) {
         if (r.interleaved) {
           turn_neighbours(a[i], c, s);
-          turn_neighbours(b[i], c + 4, s + 4);
+          turn_neighbours(b[i], c + 2, s + 2);
         } else {
           turn_halves(a[i], b[i], c, s);
         }
