@@ -33,13 +33,13 @@ constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at onc
 // Warps by role. Two warps that take the ring's slots in turn (issuers, rows)
 // need an even number of slots, so that a slot's phases are all seen by one of
 // them: a warp that had missed one could take its parity for the one it waits for.
-constexpr int kIssuer = 4, kRowsX = 6, kCodesW = 8, kCopyW = 10, kWarps = 16;  // (epilogue: 0-3)
-static_assert(kWarps - kCopyW >= 5, "warps that copy weights");
+constexpr int kIssuer = 4, kRowsX = 6, kCodesW = 8, kCopy = 10, kWarps = 12;  // (epilogue: 0-3; 11 idle)
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kABytes = kTileN * 128;
 constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
+constexpr uint32_t kSmemFew = 204 * 1024;  // few rows: leaves room beside it for small kernels before and behind
 
 struct LinearParams {
   CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
@@ -56,11 +56,11 @@ struct LinearParams {
   int stacked;           // two parts as columns of one product (few rows), else as two products
   int cols;              // columns of a product (MMA N): nt, stacked 2 nt
   int slots;             // of the ring: a K block's weights, rows and scale images each
-  int copiers;           // warps that copy weights in turn (a divisor of `slots`)
   int code_warps;        // warps that make the weights' scale images (1 or 2)
   int issuers;           // 1 or 2, each with its own accumulators
   int turns;             // one product: warps that take its rows in turn (1 or 2)
   int split;             // CTAs (a cluster) that share a tile's K
+  int early;             // the kernel before made the rows' parts: weights may be read while it runs
   uint32_t off_b, slot_b, off_img, slot_img, off_xchg, off_bar;
 };
 
@@ -193,6 +193,7 @@ __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& 
   };
   uint4 next[4];
   advance(turn);
+  if (!p.early) ptx::griddep_wait();
   if (t < p.tasks) fetch(next);
   Slot slot;
   uint8_t* base = smem + p.off_img + lane * 16;
@@ -236,6 +237,7 @@ __device__ __forceinline__ void row_codes(const LinearParams& p, const Work& w, 
   const bool wide = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.xc[part]) & 15) == 0;  // (the workspace's are aligned)
   uint8_t* base = smem + p.off_img + (1 + part * kImages) * kImg + lane * 16;
   const int g0 = w.k0 / kGroup;
+  ptx::griddep_wait();
   Codes<kImages> next;  // (of two images' rows only the present group is held)
   if (kImages == 1 && w.first < p.tasks) load_group<kImages>(p, w, part, wide, w.first, g0, next);
   Slot slot;
@@ -304,12 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem), kTmemCols);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
-  } else if (warp >= kCopyW && warp < kCopyW + p.copiers && elect_one()) {
-    // The first blocks' weights on their way to L2 (which takes nothing that
-    // the kernel before may still change) while the barriers are made.
+  } else if (warp == kCopy && elect_one()) {
+    ptx::prefetch_tmap(&p.tm_w);
     ptx::prefetch_tmap(&p.tm_x);
-    for (int k = w.k0 + warp - kCopyW; k < min(w.k1, w.k0 + p.slots) && w.first < p.tasks; k += p.copiers)
-      ptx::prefetch_tensor_3d(&p.tm_w, 0, tile_n(p, w.first), k);
   }
   __syncwarp();
   __syncthreads();
@@ -318,9 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     ptx::cluster_arrive();
     ptx::cluster_wait();
   }
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
+  if (warp == 0) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+  }
 
+  bool arrived = false;
+  // (what reads the kernel before's results waits for it in its own branch)
   if (warp >= kCodesW && warp < kCodesW + p.code_warps) {
     weight_codes(p, w, bars, smem, warp - kCodesW);
   } else if (warp >= kRowsX && warp < kRowsX + max(products, p.turns)) {
@@ -330,34 +333,44 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       row_codes<1>(p, w, bars, smem, part, turn, turns);
     else
       row_codes<2>(p, w, bars, smem, part, turn, turns);
-  } else if (warp >= kCopyW && warp < kCopyW + p.copiers) {
+  } else if (warp == kCopy) {
     // ------------------------------------------------------------ copies
     // A 4-bit box spreads its codes as the tensor cores read E2M1 rows: 16 (8
-    // bytes) in a unit of 16 bytes, whose other half is not looked at. A thread
-    // that issues tensor copies gets one through in some 400 ns, so several
-    // warps take the slots in turn.
+    // bytes) in a unit of 16 bytes, whose other half is not looked at. One
+    // thread keeps the ring full (3, 4 or 5 warps in turn: no faster).
     if (elect_one()) {
       const uint64_t keep = ptx::policy_evict_last();
       const uint64_t policy = p.tiles_m > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-      const int me = warp - kCopyW;
-      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots, turns = p.copiers;
+      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots;
       Slot slot;
-      slot.at = me;
-      int k = w.k0 + me;  // this warp's next block in the present tile
+      int k = w.k0;
+      const auto copy_w = [&](int n0, int at) {
+        ptx::mbar_arrive_expect_tx(full0 + slot.at * 8, kABytes / 2 + p.slot_b);  // (a 4-bit box counts its global bytes)
+        ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, at, full0 + slot.at * 8, policy);
+      };
+      const auto copy_x = [&](int m0, int at) {
+        ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, m0, 0, at, full0 + slot.at * 8, keep);
+      };
       bool ok = true;
+      if (w.first < p.tasks) {  // the ring's first round, all its slots empty
+        const int n0 = tile_n(p, w.first), m0 = tile_m(p, w.first), end = min(w.k1, w.k0 + static_cast<int>(R));
+        if (!p.early) ptx::griddep_wait();
+        for (int at = k; at < end; ++at, ++slot.at) copy_w(n0, at);
+        if (p.early) ptx::griddep_wait();
+        slot.at = 0;
+        for (; k < end; ++k, slot.next(R, 1)) copy_x(m0, k);
+      }
       for (int t = w.first; ok && t < p.tasks; t += w.step) {
         const int n0 = tile_n(p, t), m0 = tile_m(p, t);
-        for (; k < w.k1; k += turns, slot.next(R, turns)) {
+        for (; k < w.k1; ++k, slot.next(R, 1)) {
           if (!mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort)) {
             ok = false;
             break;
           }
-          const uint32_t full = full0 + slot.at * 8;
-          ptx::mbar_arrive_expect_tx(full, kABytes / 2 + p.slot_b);  // (a 4-bit box counts its global bytes)
-          ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, k, full, policy);
-          ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, m0, 0, k, full, keep);
+          copy_w(n0, k);
+          copy_x(m0, k);
         }
-        k += w.k0 - w.k1;
+        k = w.k0;
       }
     }
     __syncwarp();
@@ -454,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       const uint32_t d0 = lanes + acc * p.issuers * p.cols;
       const bool two = p.issuers > 1 && w.k1 - w.k0 > 1;
       const uint32_t d = d0 + (p.issuers > 1 && !two ? (lt & 1) * p.cols : 0);
-      const auto load = [&](int c0, float* v) {
+      const int sums = (two ? 2 : 1) * (p.stacked ? 2 : 1), apart = p.stacked ? p.nt : p.cols;
+      const auto load = [&](int c0, float* v) {  // the issuers' sums, and hi's and lo's, in this order
         ptx::tmem_ld_32x32b_x16(d + c0, v);
         ptx::tmem_wait_ld();
-        // the other issuer's sums, and lo's
-        for (int at = p.stacked ? p.nt : p.cols; at < (two ? 2 : 1) * p.cols; at += p.stacked ? p.nt : p.cols) {
+        for (int i = 1; i < sums; ++i) {  // (all four at once: 128 registers, and 1 us slower)
           float u[16];
-          ptx::tmem_ld_32x32b_x16(d + at + c0, u);
+          ptx::tmem_ld_32x32b_x16(d + i * apart + c0, u);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] += u[j];
@@ -516,6 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       if (lane == 0) ptx::mbar_arrive(bar(bars->tempty[acc]));
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efull), lt & 1, abort));
       if (!ok) continue;
+      if (t + w.step >= p.tasks) {  // all is sent and all has come
+        ptx::cluster_arrive();
+        arrived = true;
+      }
       if (n < p.N) {
         const float4* part = reinterpret_cast<const float4*>(smem + p.off_xchg) + tid;
         for (int c = 4 * w.rank; c < cols; c += 4 * S, part += 128) {
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 
   // ------------------------------------------------------------ teardown
   // In a cluster nobody ends before all others have sent what they send.
-  if (S > 1) ptx::cluster_arrive();
+  if (S > 1 && !arrived) ptx::cluster_arrive();
   ptx::tc_fence_before();
   __syncthreads();
   if (*abort) {
@@ -702,7 +719,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const int himg = p.cols > 128 ? 2 : 1, products = p.stacked ? 1 : p.parts;
   p.slot_b = p.parts * p.nt * 128u;
   p.slot_img = (1 + products * himg) * kImg;
-  const uint32_t fixed = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
+  const uint32_t fixed = (p.cols <= 96 ? kSmemFew : kSmemMax) - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
   const int steps = (K / 128 + kStep - 1) / kStep;
 
   // CTAs that share a tile's K: as many as the device holds at once over all
@@ -729,7 +746,6 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const uint32_t by_tmem = (kTmemCols - 2 * p.issuers * p.cols) / (4 + 4 * products * himg);
   p.slots = static_cast<int>(std::min<uint32_t>({room / (kABytes + p.slot_b + p.slot_img), by_tmem, kMaxSlots}));
   if (p.slots > 3 || p.issuers > 1) p.slots &= ~1;
-  p.copiers = p.slots % 5 == 0 ? 5 : p.slots % 4 == 0 ? 4 : p.slots % 3 == 0 ? 3 : p.slots;
   p.code_warps = p.slots >= 6 ? 2 : 1;
   p.turns = p.slots % 2 == 0 ? 2 : 1;
   if (p.slots < 2) return MOE_ERR_UNSUPPORTED;  // (no size reaches this)
@@ -739,6 +755,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.off_bar = p.off_img + p.slots * p.slot_img + (over ? 0 : xchg);
   if (over && xchg > p.off_img) return MOE_ERR_UNSUPPORTED;
 
+  p.early = x_codes == nullptr;
   const uint8_t* rows = static_cast<const uint8_t*>(x);
   int64_t row_bytes = ldx;
   p.xc[0] = x_codes;
@@ -770,7 +787,6 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemMax;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -779,6 +795,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   attr[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
+  cfg.dynamicSmemBytes = p.off_bar + sizeof(Bars) + 1024;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
