@@ -28,18 +28,20 @@ constexpr int kTileN = 128;      // weight rows of a tile (MMA M)
 constexpr int kMaxRows = 192;    // token rows of a tile (MMA N): two accumulators and the scales fit TMEM
 constexpr int kMaxSlots = 12;
 constexpr int kMaxCluster = 8;
-constexpr int kStep = 2;         // K blocks (of 128) that a weight loader takes at once: 128 bytes of a row
+constexpr int kStep = 2;         // a CTA's share of K begins at a multiple of so many K blocks (of 128)
 constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at once: 16 bytes of a row
-// Warps by role. Two warps that take the ring's slots in turn (issuers, rows)
-// need an even number of slots, so that a slot's phases are all seen by one of
-// them: a warp that had missed one could take its parity for the one it waits for.
-constexpr int kIssuer = 4, kRowsX = 6, kCodesW = 8, kCopy = 10, kWarps = 12;  // (epilogue: 0-3; 11 idle)
-constexpr int kThreads = kWarps * 32;
+// Warps by role. Several warps that take the ring's blocks in turn (issuers,
+// rows' codes) are an even number no larger than the slots', which is even too:
+// a warp's blocks then have one issuer, which frees them in order, and it has
+// seen its last one freed, less than a round before. (A warp that had missed a
+// phase of a slot could take its parity for the one it waits for.)
+// The rows' codes come last, as many warps as the launch has left.
+constexpr int kIssuer = 4, kCodesW = 6, kCopy = 8, kRowsX = 9, kMaxWarps = 13;  // (epilogue: 0-3)
+constexpr int kThreads = kMaxWarps * 32;
 constexpr uint32_t kABytes = kTileN * 128;
 constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
-constexpr uint32_t kSmemFew = 204 * 1024;  // few rows: leaves room beside it for small kernels before and behind
 
 struct LinearParams {
   CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
@@ -58,7 +60,7 @@ struct LinearParams {
   int slots;             // of the ring: a K block's weights, rows and scale images each
   int code_warps;        // warps that make the weights' scale images (1 or 2)
   int issuers;           // 1 or 2, each with its own accumulators
-  int turns;             // one product: warps that take its rows in turn (1 or 2)
+  int turns;             // one product: warps that take its rows' codes in turn (1, 2 or 4)
   int split;             // CTAs (a cluster) that share a tile's K
   int early;             // the kernel before made the rows' parts: weights may be read while it runs
   uint32_t off_b, slot_b, off_img, slot_img, off_xchg, off_bar;
@@ -169,9 +171,9 @@ __device__ __forceinline__ void store_image(uint8_t* img, const uint4 (&v)[4], i
   *reinterpret_cast<uint4*>(img) = make_uint4(word(v[0], j), word(v[1], j), word(v[2], j), word(v[3], j));
 }
 
-// The weights' scale images by two warps, groups of 4 K blocks in turn; the
-// next group's codes are on their way meanwhile. (A warp is 5 stages at most
-// behind what it last saw of the ring, which has 6 slots or more or one warp.)
+// The weights' scale images by one warp, or by two that take the groups of 4 K
+// blocks in turn (code_warps_of says when); the next group's codes are on their
+// way meanwhile.
 __device__ __forceinline__ void weight_codes(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int turn) {
   const int lane = threadIdx.x & 31, turns = p.code_warps;
   volatile int* abort = &bars->abort;
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       ptx::mbar_init(bar(bars->tfull[lane - 16]), p.issuers);
       ptx::mbar_init(bar(bars->tempty[lane - 16]), 4);
     } else if (lane == 18) {
-      ptx::mbar_init(bar(bars->efree), S);
+      ptx::mbar_init(bar(bars->efree), 4 * S);
     } else if (lane == 19) {
       ptx::mbar_init(bar(bars->efull), 1);
     } else if (lane == 20) {
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   // (what reads the kernel before's results waits for it in its own branch)
   if (warp >= kCodesW && warp < kCodesW + p.code_warps) {
     weight_codes(p, w, bars, smem, warp - kCodesW);
-  } else if (warp >= kRowsX && warp < kRowsX + max(products, p.turns)) {
+  } else if (warp >= kRowsX) {
     const int who = warp - kRowsX, part = products > 1 ? who : 0;
     const int turn = products > 1 ? 0 : who, turns = products > 1 ? 1 : p.turns;
     if (himg == 1)
@@ -497,11 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
       // Columns 4 c .. 4 c + 3 of the tile are summed by the CTA c % S: every CTA
       // sends its parts of the columns to their CTAs, and adds up those it gets
-      // in the order of the ranks. Where a buffer lies over the ring, or still
-      // holds the last tile's parts, its CTA first says that it is free (all
-      // MMAs are done, the sums are read).
+      // in the order of the ranks. Its warps say when the buffer is free: over
+      // the ring, when all MMAs are done; else when the last tile's sums are read.
+      if (over && lane < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), lane));
       if (over || lt > 0) {
-        if (tid < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), tid));
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar(bars->efree), (over ? 0 : lt - 1) & 1, abort));
         if (!ok) continue;
       }
@@ -550,6 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           if (c + 2 < cols) o[2 * p.ldo] = __float2bfloat16_rn(sum.z);
           if (c + 3 < cols) o[3 * p.ldo] = __float2bfloat16_rn(sum.w);
         }
+      }
+      if (!over && t + w.step < p.tasks) {
+        __syncwarp();
+        if (lane < S) ptx::mbar_arrive_cluster(ptx::cluster_addr(bar(bars->efree), lane));
       }
     }
   }
@@ -635,6 +640,14 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams p) {
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
 
+// Two warps may make the weights' scale images in turn, by groups of 4 K blocks,
+// where for each block that one of them waits for it has waited for one of the
+// same issuer's (an even number of blocks before) less than a round, `slots`
+// blocks, ago. Between a warp's groups lie 4 blocks at most: its last group's
+// last two are 5 and 6 before, or where that one has a single block (a tile's
+// last, 4 i + 1 blocks of K) that is 5 before and the one of the same issuer 10.
+int code_warps_of(int slots, int nk) { return slots >= 10 || (slots >= 6 && nk % 4 != 1) ? 2 : 1; }
+
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // How many clusters of each size the device holds at once (looked up once per device).
@@ -719,7 +732,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const int himg = p.cols > 128 ? 2 : 1, products = p.stacked ? 1 : p.parts;
   p.slot_b = p.parts * p.nt * 128u;
   p.slot_img = (1 + products * himg) * kImg;
-  const uint32_t fixed = (p.cols <= 96 ? kSmemFew : kSmemMax) - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
+  const uint32_t fixed = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
   const int steps = (K / 128 + kStep - 1) / kStep;
 
   // CTAs that share a tile's K: as many as the device holds at once over all
@@ -746,8 +759,10 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const uint32_t by_tmem = (kTmemCols - 2 * p.issuers * p.cols) / (4 + 4 * products * himg);
   p.slots = static_cast<int>(std::min<uint32_t>({room / (kABytes + p.slot_b + p.slot_img), by_tmem, kMaxSlots}));
   if (p.slots > 3 || p.issuers > 1) p.slots &= ~1;
-  p.code_warps = p.slots >= 6 ? 2 : 1;
-  p.turns = p.slots % 2 == 0 ? 2 : 1;
+  p.code_warps = code_warps_of(p.slots, K / 128);
+  // (four warps where a CTA has whole tiles to stream: 129281 columns of 5120, 7 rows
+  // 56 us, with two 59)
+  p.turns = p.slots % 2 ? 1 : p.slots >= 6 && split == 1 ? 4 : 2;
   if (p.slots < 2) return MOE_ERR_UNSUPPORTED;  // (no size reaches this)
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
@@ -786,7 +801,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32u * (kRowsX + (products > 1 ? products : p.turns)));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
