@@ -12,4 +12,4 @@ attention side's argument marshalling (csrc/host.cpp) in-tree.
 from .api import MoeDecode, attn_seam_x8, expected_shapes, kernel_names  # noqa: F401
 from .attention import (add_norm_x8, attn_x8, attn_x8_workspace, kv_append_x8,  # noqa: F401
                         kv_cache_x8, kv_dequant_x8, norm_add_norm_x8, rope, rope_freqs, rope_kv_append_x8)
-from .linear import linear_x4, linear_x4_workspace_bytes  # noqa: F401
+from .linear import dequant_x4, linear_x4, linear_x4_workspace_bytes, quant_x4  # noqa: F401

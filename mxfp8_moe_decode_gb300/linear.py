@@ -5,6 +5,8 @@ Argument marshalling only, in compiled code, as :mod:`.attention`.
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import attention, _lib
@@ -26,6 +28,34 @@ def linear_x4(x: torch.Tensor, w: torch.Tensor, w_codes: torch.Tensor, x_codes: 
     """
     return _result((attention._bound or attention._host()).linear_x4(x, w, w_codes, x_codes, out, workspace, status),
                    "moe_linear_x4")
+
+
+def quant_x4(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """(uint8 [N, K / 2], uint8 [N, K / 32]) of weights [N, K] in MXFP4 (torch
+    operations, any device): per 32 columns the smallest scale 2^(code - 127) under
+    which no value passes E2M1's largest, 6, and the nearest E2M1 values, ties to
+    the even code. For finite weights; K a multiple of 32."""
+    if w.dim() != 2 or w.shape[1] % 32:
+        raise ValueError(f"w must be [N, K] with K a multiple of 32, got {tuple(w.shape)}")
+    groups = w.double().view(w.shape[0], -1, 32)
+    m, e = torch.frexp(groups.abs().amax(-1) / 6.0)
+    code = (torch.where(m == 0.5, e - 1, e) + 127).clamp(0, 254) * (m > 0)  # a group of zeros: 0
+    v = groups * torch.exp2(127.0 - code.double())[..., None]
+    # the borders between E2M1's values; at .75, 1.75 and 3.5 the even code is the upper one
+    border = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+    border = [math.nextafter(b, 0.0) if b in (0.75, 1.75, 3.5) else b for b in border]
+    nibble = torch.bucketize(v.abs().contiguous(), torch.tensor(border, dtype=torch.float64, device=w.device))
+    nibble = (nibble + 8 * torch.signbit(v)).to(torch.uint8).view(w.shape[0], -1, 2)
+    return nibble[..., 0] | (nibble[..., 1] << 4), code.to(torch.uint8)
+
+
+def dequant_x4(w: torch.Tensor, w_codes: torch.Tensor) -> torch.Tensor:
+    """The values that MXFP4 rows stand for, fp32 [N, K] (for tests and
+    inspection: torch operations, any device)."""
+    table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=w.device)
+    table = torch.cat((table, -table))
+    v = torch.stack((table[(w & 15).long()], table[(w >> 4).long()]), -1).view(w.shape[0], -1, 32)
+    return (v.double() * torch.exp2(w_codes.double() - 127)[..., None]).float().view(w.shape[0], -1)
 
 
 def linear_x4_workspace_bytes(rows: int, cols: int, mxfp8: bool) -> int:

@@ -6,8 +6,11 @@ import math
 import numpy as np
 import pytest
 
-from mxfp8_moe_decode_gb300 import rope_freqs
+import torch
+
+from mxfp8_moe_decode_gb300 import dequant_x4, quant_x4, rope_freqs
 from oracle import layer as L
+from oracle.mx import dequant_fp4_rows
 
 
 def test_block_residual():
@@ -85,3 +88,34 @@ def test_rope_freqs_by_parts():
 def test_rope_freqs_refusals(kw):
     with pytest.raises(ValueError):
         rope_freqs(device="cpu", **kw)
+
+
+def test_quant_x4_rounds_to_the_nearest():
+    """Every E2M1 border from both sides and on it, under scales far apart, and groups of zeros."""
+    values = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+    tie = {0.25: 0.0, 0.75: 1.0, 1.25: 1.0, 1.75: 2.0, 2.5: 2.0, 3.5: 4.0, 5.0: 4.0}
+    row, want = [], []
+    for b, t in tie.items():
+        lo, hi = max(v for v in values if v < b), min(v for v in values if v > b)
+        for x, y in ((b - 1e-6, lo), (b, t), (b + 1e-6, hi)):
+            row += [x, -x]
+            want += [y, -y]
+    row, want = row[:31] + [6.0], want[:31] + [6.0]
+    rows = torch.tensor([row, row, [0.0] * 32], dtype=torch.float64) * torch.tensor([[1.0], [2.0 ** -60], [1.0]], dtype=torch.float64)
+    w, c = quant_x4(rows)
+    assert c.tolist() == [[127], [67], [0]]
+    got = dequant_x4(w, c).double()
+    assert got[0].tolist() == want and (got[1] * 2.0 ** 60).tolist() == want and not got[2].any()
+    assert np.array_equal(dequant_fp4_rows(w.numpy(), c.numpy()), got.numpy())
+
+
+def test_quant_x4_takes_the_smallest_scale():
+    w = torch.zeros(3, 64, dtype=torch.bfloat16)
+    w[0, 3], w[0, 40], w[1, 0], w[2, 63] = 6.0, -6.03125, 3.0, 1e-30
+    packed, c = quant_x4(w)
+    assert c.tolist()[0] == [127, 128] and c.tolist()[1] == [126, 0]
+    d = dequant_x4(packed, c)
+    assert d[0, 3] == 6.0 and d[0, 40] == -6.0 and d[1, 0] == 3.0 and abs(d[2, 63].item() / 1e-30 - 1) < 0.25
+    assert packed.shape == (3, 32)
+    with pytest.raises(ValueError):
+        quant_x4(w[:, :40])
