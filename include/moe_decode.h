@@ -599,11 +599,25 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
  *           else E4M3 bytes [M, K], rows ldx bytes apart (a multiple of 16), with
  *           x_codes u8 [M, K/32] (contiguous, 4-byte aligned): MXFP8 rows as
  *           moe_add_norm_x8 writes them. 16-byte aligned
- *  out      bf16 [M, N], rows ldo elements apart (any ldo >= N)
+ *  out      bf16 [M, N], rows ldo elements apart (any ldo >= N); what lies between
+ *           the rows stays. out overlaps no other operand
  *  status   int32 (device, 4-byte aligned) or null: MOE_LINEAR_STATUS_TIMEOUT is set
  *           where a bounded wait expired (out is unspecified then)
  * The weights are read as they are: nothing is laid out before, nothing is kept.
- * Products are exact and sums fp32.
+ * Products are exact and sums fp32, with the one rounding of out; results do not
+ * change from run to run (the order of a sum depends on M, N, K and the GPU). bf16 rows are multiplied as two MXFP8 rows, exact for
+ * values down to 2^-14 of the largest of their 32 columns and off by at most 2^-21
+ * of that largest below. A value of x that is not finite (a byte 0x7F or 0xFF, a
+ * code 255) makes its row of out NaN, and no other.
+ *
+ * workspace: for bf16 rows only (else null will do): device memory, 16-byte
+ * aligned, of at least moe_linear_x4_workspace_bytes(M, K, MOE_LINEAR_BF16); it
+ * needs no initial state. Calls that may overlap on the GPU, captured ones among
+ * them, need workspaces of their own. One kernel on `stream` (bf16 rows: two); no
+ * allocation, no synchronisation, capture safe. Errors: MOE_ERR_RANGE (M < 0 or >
+ * 2^20, N < 0 or > 2^24), MOE_ERR_UNSUPPORTED (K not a multiple of 128 in [128,
+ * 65536]), MOE_ERR_ARG (null, a stride below its row, a workspace that is too
+ * small), MOE_ERR_ALIGN, MOE_ERR_CUDA. M = 0 or N = 0 enqueues nothing.
  */
 #define MOE_LINEAR_BF16 0
 #define MOE_LINEAR_MXFP8 1

@@ -719,9 +719,8 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.parts = x_codes ? 1 : 2;
   p.tiles_m = (M + kMaxRows - 1) / kMaxRows;
   p.nt = round_up((M + p.tiles_m - 1) / p.tiles_m, 16);
-  const int64_t tasks = static_cast<int64_t>((N + kTileN - 1) / kTileN) * p.tiles_m;
-  if (tasks > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  p.tasks = static_cast<int>(tasks);
+  p.tasks = (N + kTileN - 1) / kTileN * p.tiles_m;  // (fits: below 2^30)
+  const int64_t tasks = p.tasks;
   // bf16 rows: a product of 32 to 64 columns takes the time of one of 16, so few
   // rows' two parts are columns of one product; the products of more are two
   // that share their scales' copies and weights.
@@ -735,6 +734,8 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   const uint32_t fixed = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
   const int steps = (K / 128 + kStep - 1) / kStep;
 
+  // The ring (227 KB over 19 to 67 KB a slot) has 3 slots at least, more than the
+  // exchange buffer that may lie over it (96 KB at most).
   // CTAs that share a tile's K: as many as the device holds at once over all
   // tiles, while each has some stages to itself; shares of one task a cluster
   // only, or with an exchange buffer beside the ring.
@@ -763,12 +764,10 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   // (four warps where a CTA has whole tiles to stream: 129281 columns of 5120, 7 rows
   // 56 us, with two 59)
   p.turns = p.slots % 2 ? 1 : p.slots >= 6 && split == 1 ? 4 : 2;
-  if (p.slots < 2) return MOE_ERR_UNSUPPORTED;  // (no size reaches this)
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
   p.off_xchg = over ? 0 : p.off_img + p.slots * p.slot_img;
   p.off_bar = p.off_img + p.slots * p.slot_img + (over ? 0 : xchg);
-  if (over && xchg > p.off_img) return MOE_ERR_UNSUPPORTED;
 
   p.early = x_codes == nullptr;
   const uint8_t* rows = static_cast<const uint8_t*>(x);
