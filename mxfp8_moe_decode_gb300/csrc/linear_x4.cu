@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kTileN = 128;      // weight rows of a tile (MMA M)
 constexpr int kMaxRows = 192;    // token rows of a tile (MMA N): two accumulators and the scales fit TMEM
+constexpr int kMaxTasks = 1 << 30;
 constexpr int kMaxSlots = 12;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 2;         // a CTA's share of K begins at a multiple of so many K blocks (of 128)
@@ -60,6 +61,7 @@ struct LinearParams {
   int slots;             // of the ring: a K block's weights, rows and scale images each
   int code_warps;        // warps that make the weights' scale images (1 or 2)
   int issuers;           // 1 or 2, each with its own accumulators
+  int accs;              // of an issuer: 2 in turn, or 1 where a CTA has one tile only
   int turns;             // one product: warps that take its rows' codes in turn (1, 2 or 4)
   int split;             // CTAs (a cluster) that share a tile's K
   int early;             // the kernel before made the rows' parts: weights may be read while it runs
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       // himg of each product's rows. (The products take them from a column that
       // is a multiple of 4 only.)
       const uint32_t sfx = 4 * himg, sf_slot = 4 + products * sfx;
-      const uint32_t sf0 = tmem + 2 * p.issuers * p.cols;
+      const uint32_t sf0 = tmem + p.accs * p.issuers * p.cols;
       const uint32_t part_units = static_cast<uint32_t>(p.nt) * 8u;  // of 16 bytes, as descriptors count
       const uint32_t idesc = ptx::idesc_mxf8(p.cols, 0, ptx::kFmtE2M1), idesc_k = ptx::idesc_mxf8(0, 1, 0) - ptx::idesc_mxf8(0, 0, 0);
       const uint64_t a0 = ptx::sdesc_k128_sw128(sbase), b0 = ptx::sdesc_k128_sw128(sbase + p.off_b),
@@ -675,6 +677,83 @@ int max_clusters(int device, int split) {
   return n;
 }
 
+// How a product is laid out over the GPU, and what that takes.
+struct Shape {
+  int nt, tiles_m;  // token rows of a tile, and such tiles
+  int64_t tasks;
+  bool stacked;
+  int cols, products, himg;
+  int split, clusters;
+  bool over;  // the exchange buffer lies over the ring (one tile a cluster)
+  uint32_t xchg;
+  int accs, issuers, slots;
+  int64_t ns;  // estimate, without what all shapes have alike
+};
+
+// The shape for tiles of up to nt token rows and K shared by `split` CTAs, of
+// which the device holds `clusters` clusters; false where it does not work.
+bool shape_of(int M, int N, int K, int parts, int nt, int split, int clusters, Shape& s) {
+  s.tiles_m = (M + nt - 1) / nt;
+  const int per_tile = (M + s.tiles_m - 1) / s.tiles_m;
+  // Few rows' hi and lo are columns of one product (one of 32 to 64 columns takes
+  // the time of one of 16), more rows' two that share the weights and their scales.
+  s.stacked = parts == 2 && per_tile <= 64;
+  s.nt = round_up(per_tile, s.stacked ? 8 : 16);
+  s.products = s.stacked ? 1 : parts;
+  s.cols = s.stacked ? 2 * s.nt : s.nt;
+  s.himg = s.cols > 128 ? 2 : 1;
+  s.tasks = static_cast<int64_t>((N + kTileN - 1) / kTileN) * s.tiles_m;
+  s.split = split;
+  s.clusters = clusters;
+  if (s.tasks > kMaxTasks || (split > 1 && s.tasks > clusters && s.nt > 64)) return false;
+  s.over = split > 1 && s.nt > 64;
+  s.xchg = split > 1 ? static_cast<uint32_t>(round_up(s.nt / 4, split)) * 2048u : 0;
+  s.accs = s.tasks > clusters ? 2 : 1;
+  // Two issuers where their accumulators and a ring of 4 slots (all even, see
+  // above) fit: 300 MXFP8 rows of 5120 to 7168 columns, 160 a tile: 16.4 us with
+  // two, 20.3 with one; bf16 rows alike, on a ring of 2 slots in place of 3, 33.1 and 28.7.
+  const uint32_t room = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64 - (s.over ? 0 : s.xchg);
+  const uint32_t slot = kABytes + parts * s.nt * 128u + (1 + s.products * s.himg) * kImg;
+  for (s.issuers = 2;; s.issuers = 1) {
+    const int tmem = static_cast<int>(kTmemCols) - s.accs * s.issuers * s.cols;
+    s.slots = std::min({static_cast<int>(room / slot), tmem / (4 + 4 * s.products * s.himg), kMaxSlots});
+    if (s.slots >= 4 || s.issuers == 1) break;
+  }
+  if (s.slots > 3) s.slots &= ~1;
+  // The estimate: a K block's time (a line through measured ones of 48 to 384
+  // columns; one issuer takes 340 ns and more, with two products 500), what a
+  // tile's columns cost at its end, and what it costs to share K: an exchange,
+  // behind which a CTA's next tile hides from some 4 us on. (48 rows, 5120
+  // columns to 27648, three tiles a pair: 18.3 us, with whole tiles 19.5; to 7168,
+  // one tile a pair 9.4, two tiles five CTAs 10.9.)
+  int64_t block = 110 + 5 * s.products * s.cols / 4;
+  if (s.issuers == 1) block = std::max<int64_t>(block, 180 + 160 * s.products);
+  const int steps = (K / 128 + kStep - 1) / kStep;
+  const int64_t tiles = (s.tasks + clusters - 1) / clusters, tile = (steps + split - 1) / split * kStep * block + 10 * s.nt;
+  s.ns = split == 1 ? tiles * tile : (tiles - 1) * std::max<int64_t>(tile, 4000) + tile + 1500 + 5 * s.nt;
+  return true;
+}
+
+// The shape of the smallest estimate. (5120 columns to 7168, MXFP8: 400 rows in
+// five tiles of 80 rows 20.2 us, in three of 144 as few as can be 32.1; 192 rows
+// of 2048 to 2048 in six tiles of 32 7.2, in one with K shared by four CTAs 8.9.)
+bool choose_shape(int M, int N, int K, int parts, int device, Shape& best) {
+  const int steps = (K / 128 + kStep - 1) / kStep;
+  bool any = false;
+  for (int nt = kMaxRows, tiles = 0; nt > 0; nt -= 16) {
+    if ((M + nt - 1) / nt == tiles) continue;  // (the last one's tiles, as even as they get)
+    tiles = (M + nt - 1) / nt;
+    for (int split = 1; split <= std::min(kMaxCluster, steps); ++split) {
+      Shape s;
+      const int clusters = max_clusters(device, split);
+      if (clusters == 0 || !shape_of(M, N, K, parts, nt, split, clusters, s)) continue;
+      if (!any || s.ns < best.ns) best = s;
+      any = true;
+    }
+  }
+  return any;
+}
+
 // One part's codes in the workspace.
 size_t split_codes(int M, int K) { return (static_cast<size_t>(M) * K / 32 + 15) / 16 * 16; }
 
@@ -717,57 +796,30 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.N = N;
   p.K = K;
   p.parts = x_codes ? 1 : 2;
-  p.tiles_m = (M + kMaxRows - 1) / kMaxRows;
-  p.nt = round_up((M + p.tiles_m - 1) / p.tiles_m, 16);
-  p.tasks = (N + kTileN - 1) / kTileN * p.tiles_m;  // (fits: below 2^30)
-  const int64_t tasks = p.tasks;
-  // bf16 rows: a product of 32 to 64 columns takes the time of one of 16, so few
-  // rows' two parts are columns of one product; the products of more are two
-  // that share their scales' copies and weights.
-  p.stacked = p.parts == 2 && p.nt <= 64;
-  if (p.stacked) p.nt = round_up(M, 8);
-  p.cols = p.stacked ? 2 * p.nt : p.nt;
-  p.issuers = p.cols <= 96 ? 2 : 1;  // (their accumulators fit TMEM; the time of wider products hides the issue)
-  const int himg = p.cols > 128 ? 2 : 1, products = p.stacked ? 1 : p.parts;
-  p.slot_b = p.parts * p.nt * 128u;
-  p.slot_img = (1 + products * himg) * kImg;
-  const uint32_t fixed = kSmemMax - 1024 - static_cast<uint32_t>(sizeof(Bars)) - 64;
-  const int steps = (K / 128 + kStep - 1) / kStep;
-
-  // The ring (227 KB over 19 to 67 KB a slot) has 3 slots at least, more than the
-  // exchange buffer that may lie over it (96 KB at most).
-  // CTAs that share a tile's K: as many as the device holds at once over all
-  // tiles, while each has some stages to itself; shares of one task a cluster
-  // only, or with an exchange buffer beside the ring.
-  int split = 1, clusters = max_clusters(device, 1);
-  if (clusters == 0) return MOE_ERR_CUDA;
-  const auto cost = [&](int s, int c) { return (tasks + c - 1) / c * ((steps + s - 1) / s * kStep + (s > 1 ? 6 : 3)); };
-  int64_t best = cost(1, clusters);
-  for (int s = 2; s <= kMaxCluster && s <= steps; ++s) {
-    const int c = max_clusters(device, s);
-    if (c == 0 || (tasks > c && p.nt > 64)) continue;
-    if (cost(s, c) < best) {
-      best = cost(s, c);
-      split = s;
-      clusters = c;
-    }
-  }
+  Shape shape;
+  if (!choose_shape(M, N, K, p.parts, device, shape)) return MOE_ERR_CUDA;
+  const int products = shape.products, split = shape.split;
+  const int clusters = static_cast<int>(std::min<int64_t>(shape.clusters, shape.tasks));
+  p.tiles_m = shape.tiles_m;
+  p.nt = shape.nt;
+  p.tasks = static_cast<int>(shape.tasks);
+  p.stacked = shape.stacked;
+  p.cols = shape.cols;
+  p.issuers = shape.issuers;
+  p.accs = shape.accs;
+  p.slots = shape.slots;
   p.split = split;
-  clusters = std::min(clusters, p.tasks);
-  const uint32_t xchg = split > 1 ? static_cast<uint32_t>((p.nt / 4 + split - 1) / split * split) * 2048u : 0;
-  const bool over = split > 1 && p.nt > 64;  // the exchange buffer lies over the ring (one tile a cluster)
-  const uint32_t room = fixed - (over ? 0 : xchg);
-  const uint32_t by_tmem = (kTmemCols - 2 * p.issuers * p.cols) / (4 + 4 * products * himg);
-  p.slots = static_cast<int>(std::min<uint32_t>({room / (kABytes + p.slot_b + p.slot_img), by_tmem, kMaxSlots}));
-  if (p.slots > 3 || p.issuers > 1) p.slots &= ~1;
+  p.slot_b = p.parts * p.nt * 128u;
+  p.slot_img = (1 + products * shape.himg) * kImg;
   p.code_warps = code_warps_of(p.slots, K / 128);
   // (four warps where a CTA has whole tiles to stream: 129281 columns of 5120, 7 rows
   // 56 us, with two 59)
   p.turns = p.slots % 2 ? 1 : p.slots >= 6 && split == 1 ? 4 : 2;
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
-  p.off_xchg = over ? 0 : p.off_img + p.slots * p.slot_img;
-  p.off_bar = p.off_img + p.slots * p.slot_img + (over ? 0 : xchg);
+  // (a ring has 3 slots at least, more than the 96 KB that an exchange buffer over it takes)
+  p.off_xchg = shape.over ? 0 : p.off_img + p.slots * p.slot_img;
+  p.off_bar = p.off_img + p.slots * p.slot_img + (shape.over ? 0 : shape.xchg);
 
   p.early = x_codes == nullptr;
   const uint8_t* rows = static_cast<const uint8_t*>(x);
