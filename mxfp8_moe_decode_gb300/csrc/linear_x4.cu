@@ -37,8 +37,8 @@ constexpr int kGroup = 4;        // K blocks whose scale codes are loaded at onc
 // seen its last one freed, less than a round before. (A warp that had missed a
 // phase of a slot could take its parity for the one it waits for.)
 // The rows' codes come last, as many warps as the launch has left.
-constexpr int kIssuer = 4, kCodesW = 6, kCopy = 8, kRowsX = 9, kMaxWarps = 13;  // (epilogue: 0-3)
-constexpr int kThreads = kMaxWarps * 32;
+constexpr int kIssuer = 4, kCodesW = 6, kCopy = 8, kRowsX = 9;  // (epilogue: 0-3)
+constexpr int threads_of(bool raw) { return 32 * (kRowsX + (raw ? 8 : 4)); }  // at most
 constexpr uint32_t kABytes = kTileN * 128;
 constexpr uint32_t kImg = 512;   // scale image of 128 rows and one K block
 constexpr uint32_t kTmemCols = 512;
@@ -70,6 +70,7 @@ struct LinearParams {
 
 struct Bars {
   uint64_t full[kMaxSlots];   // a K block's weights, rows and images are there
+  uint64_t raw[kMaxSlots];    // its bf16 rows are there
   uint64_t empty[kMaxSlots];  // its MMAs have read them
   uint64_t tfull[2], tempty[2];
   uint64_t efree;             // every CTA of the cluster has its exchange buffer free
@@ -276,7 +277,95 @@ __device__ __forceinline__ void row_codes(const LinearParams& p, const Work& w, 
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
+// A K block's bf16 rows in a slot, in place, to its hi and lo rows, and their
+// images. The copy brings every row as two halves of 64 columns, hi's bytes of a
+// row come where the first half was, lo's where the second was: 8 rows a step,
+// a lane a row's 32 columns of one code.
+__device__ __forceinline__ void split_block(uint8_t* b, uint8_t* img, int nt, int rows, int first) {
+  const int lane = threadIdx.x & 31, r = lane & 7, g = lane >> 3;  // (so 8 lanes' chunks lie in 8 columns of banks)
+  for (int row = first + r; row < rows + r; row += 16) {
+    const uint8_t* from = b + ((g >> 1) * nt + row) * 128;
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(from + (((g & 1) * 4 + j) ^ r) * 16);
+      w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+    }
+    __syncwarp();
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+    if (__any_sync(0xffffffffu, max(top >> 16, top & 0xFFFFu) >= 0x7F80u)) {  // values that are not finite: NaN, and not looked at
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t m = w[j] & 0x7FFF7FFFu, finite = __vcmpltu2(m, 0x7F807F80u);
+        top = __vmaxu2(top, m & finite);
+        w[j] = (w[j] & finite) | (0x7FFF7FFFu & ~finite);
+      }
+    }
+    // (rows past the last, zeros, some code: the division by 448 is slow at the smallest values)
+    const int code = mx_code(row < rows ? __uint_as_float(max(top >> 16, top & 0xFFFFu) << 16) : 1.0f), low = max(code - 4, 0);
+    const float mul = mx_mul(code);
+    const __half2 up = __float2half2_rn(static_cast<float>(1 << (code - low)));
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t h2[2], l2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = w[2 * j + i];
+        // (f16 holds what the two parts can: 448 and below, in steps of 2^-24)
+        const __half2 v = __floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xFFFF0000u) * mul);
+        const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
+        const __half2 rest = __hmul2(__hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3))), up);
+        h2[i] = h;
+        l2[i] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
+      }
+      hi[j] = h2[0] | (h2[1] << 16);
+      lo[j] = l2[0] | (l2[1] << 16);
+    }
+    uint8_t* to = b + row * 128;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = ((2 * g + i) ^ r) * 16;
+      *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      *reinterpret_cast<uint4*>(to + nt * 128 + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+    const int c = nt + row;
+    img[(row & 31) * 16 + (row >> 5) * 4 + g] = static_cast<uint8_t>(code);
+    img[(c & 31) * 16 + (c >> 5) * 4 + g] = static_cast<uint8_t>(low);
+  }
+}
+
+// The bf16 rows' warps, which take the blocks in turn.
+__device__ __forceinline__ void split_rows(const LinearParams& p, const Work& w, Bars* bars, uint8_t* smem, int who) {
+  const int turn = who >> 1;
+  volatile int* abort = &bars->abort;
+  const uint32_t empty0 = ptx::smem_u32(bars->empty), full0 = ptx::smem_u32(bars->full), raw0 = ptx::smem_u32(bars->raw),
+                 R = p.slots;
+  Slot slot;
+  slot.at = turn;
+  int k = w.k0 + turn;
+  for (int t = w.first; t < p.tasks; t += w.step) {
+    const int rows = min(p.M - tile_m(p, t), p.nt);
+    for (; k < w.k1; k += p.turns, slot.next(R, p.turns)) {
+      // (the slot is free, so its copy before has come: the other phase of that parity cannot be taken for this one)
+      const bool ok = mbar_wait_clocks(empty0 + slot.at * 8, slot.phase ^ 1, abort) &&
+                      mbar_wait_clocks(raw0 + slot.at * 8, slot.phase, abort);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      split_block(smem + p.off_b + slot.at * p.slot_b, smem + p.off_img + slot.at * p.slot_img + kImg, p.nt, rows, 8 * (who & 1));
+      __syncwarp();
+      if (elect_one()) ptx::mbar_arrive(full0 + slot.at * 8);
+    }
+    k += w.k0 - w.k1;
+  }
+}
+
+// kRaw: the copies bring bf16 rows, and the kernel takes them apart itself. (One
+// kernel for both: 7 rows, 129281 columns 64 us in place of 57.)
+template <bool kRaw>
+__global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
   const uint32_t sbase = ptx::smem_u32(smem);
@@ -291,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 
   if (warp == 0) {
     if (lane < kMaxSlots) {
-      ptx::mbar_init(bar(bars->full[lane]), 2 + products);  // the copies, the weights' images, each product's rows'
+      ptx::mbar_init(bar(bars->full[lane]), 2 + (kRaw ? 2 : products));  // the copies, the weights' images, each product's rows'
+      if (kRaw) ptx::mbar_init(bar(bars->raw[lane]), 1);
       ptx::mbar_init(bar(bars->empty[lane]), 1);
     } else if (lane >= 16 && lane < 18) {
       ptx::mbar_init(bar(bars->tfull[lane - 16]), p.issuers);
@@ -333,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   } else if (warp >= kRowsX) {
     const int who = warp - kRowsX, part = products > 1 ? who : 0;
     const int turn = products > 1 ? 0 : who, turns = products > 1 ? 1 : p.turns;
-    if (himg == 1)
+    if (kRaw)
+      split_rows(p, w, bars, smem, who);
+    else if (himg == 1)
       row_codes<1>(p, w, bars, smem, part, turn, turns);
     else
       row_codes<2>(p, w, bars, smem, part, turn, turns);
@@ -345,14 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     if (elect_one()) {
       const uint64_t keep = ptx::policy_evict_last();
       const uint64_t policy = p.tiles_m > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), R = p.slots;
+      const uint32_t empty0 = bar(bars->empty[0]), full0 = bar(bars->full[0]), raw0 = bar(bars->raw[0]), R = p.slots;
       Slot slot;
       int k = w.k0;
       const auto copy_w = [&](int n0, int at) {
-        ptx::mbar_arrive_expect_tx(full0 + slot.at * 8, kABytes / 2 + p.slot_b);  // (a 4-bit box counts its global bytes)
+        ptx::mbar_arrive_expect_tx(full0 + slot.at * 8, kABytes / 2 + (kRaw ? 0 : p.slot_b));  // (a 4-bit box counts its global bytes)
         ptx::tma_load_3d(sbase + slot.at * kABytes, &p.tm_w, 0, n0, at, full0 + slot.at * 8, policy);
       };
       const auto copy_x = [&](int m0, int at) {
+        if (kRaw) {
+          ptx::mbar_arrive_expect_tx(raw0 + slot.at * 8, p.slot_b);
+          ptx::tma_load_3d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, m0, 2 * at, raw0 + slot.at * 8, keep);
+          return;
+        }
         ptx::tma_load_4d(sbase + p.off_b + slot.at * p.slot_b, &p.tm_x, 0, m0, 0, at, full0 + slot.at * 8, keep);
       };
       bool ok = true;
@@ -659,17 +756,18 @@ int max_clusters(int device, int split) {
   if (device < 0 || device >= kDevices) return 0;
   int n = known[device][split].load(std::memory_order_relaxed);
   if (n > 0) return n;
-  if (cudaFuncSetAttribute(linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess) return 0;
+  for (const void* f : {reinterpret_cast<const void*>(linear_kernel<false>), reinterpret_cast<const void*>(linear_kernel<true>)})
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(true));
   cfg.dynamicSmemBytes = kSmemMax;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<true>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -687,6 +785,7 @@ struct Shape {
   bool over;  // the exchange buffer lies over the ring (one tile a cluster)
   uint32_t xchg;
   int accs, issuers, slots;
+  bool raw;  // the kernel takes the bf16 rows apart itself
   int64_t ns;  // estimate, without what all shapes have alike
 };
 
@@ -730,6 +829,13 @@ bool shape_of(int M, int N, int K, int parts, int nt, int split, int clusters, S
   if (s.issuers == 1) block = std::max<int64_t>(block, 180 + 160 * s.products);
   const int steps = (K / 128 + kStep - 1) / kStep;
   const int64_t tiles = (s.tasks + clusters - 1) / clusters, tile = (steps + split - 1) / split * kStep * block + 10 * s.nt;
+  // A kernel in front that takes bf16 rows apart costs some 1.5 us; the warps that
+  // do it here, 8 rows of a K block a step, are the slower the more rows a CTA
+  // goes through. To 5120 columns from 5120 (14 blocks a CTA): 1 row 8.1 us here,
+  // 8.8 with a kernel in front, 16 rows (224) 8.7 and 9.4, 24 (336) 10.2 and 9.8,
+  // 48 12.9 and 10.9; 16 rows of 2048 to 2048 (64) 4.8 and 6.6, 16 rows of 5120 to
+  // 7168 (320) 9.8 and 10.3, 17 rows of 1024 to 60000 (768) 15.5 and 13.2.
+  s.raw = s.stacked && tiles * ((steps + split - 1) / split) * kStep * s.nt <= 320;
   s.ns = split == 1 ? tiles * tile : (tiles - 1) * std::max<int64_t>(tile, 4000) + tile + 1500 + 5 * s.nt;
   return true;
 }
@@ -814,18 +920,18 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.code_warps = code_warps_of(p.slots, K / 128);
   // (four warps where a CTA has whole tiles to stream: 129281 columns of 5120, 7 rows
   // 56 us, with two 59)
-  p.turns = p.slots % 2 ? 1 : p.slots >= 6 && split == 1 ? 4 : 2;
+  p.turns = p.slots % 2 ? 1 : (p.slots >= 6 && split == 1) || (shape.raw && p.slots >= 4) ? 4 : 2;
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
   // (a ring has 3 slots at least, more than the 96 KB that an exchange buffer over it takes)
   p.off_xchg = shape.over ? 0 : p.off_img + p.slots * p.slot_img;
   p.off_bar = p.off_img + p.slots * p.slot_img + (shape.over ? 0 : shape.xchg);
 
-  p.early = x_codes == nullptr;
+  p.early = !x_codes && !shape.raw;
   const uint8_t* rows = static_cast<const uint8_t*>(x);
   int64_t row_bytes = ldx;
   p.xc[0] = x_codes;
-  if (!x_codes) {
+  if (p.early) {
     SplitParams q;
     q.x = static_cast<const __nv_bfloat16*>(x);
     q.ldx = ldx;
@@ -846,13 +952,14 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
     }
   }
   if (!encode_blocks(&p.tm_w, w, true, K, N, K / 2, 0, 0, kTileN, 1)) return MOE_ERR_CUDA;
-  if (!encode_blocks(&p.tm_x, rows, false, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K,
-                     p.nt, p.parts))
-    return MOE_ERR_CUDA;
+  const bool encoded =
+      shape.raw ? encode_blocks(&p.tm_x, x, false, 2 * static_cast<uint64_t>(K), M, 2 * ldx, 0, 0, p.nt, 2)
+            : encode_blocks(&p.tm_x, rows, false, K, M, row_bytes, p.parts, static_cast<uint64_t>(M) * K, p.nt, p.parts);
+  if (!encoded) return MOE_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
-  cfg.blockDim = dim3(32u * (kRowsX + (products > 1 ? products : p.turns)));
+  cfg.blockDim = dim3(32u * (kRowsX + (products > 1 ? products : shape.raw ? 2 * p.turns : p.turns)));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -862,7 +969,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
   cfg.dynamicSmemBytes = p.off_bar + sizeof(Bars) + 1024;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shape.raw ? linear_kernel<true> : linear_kernel<false>, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
