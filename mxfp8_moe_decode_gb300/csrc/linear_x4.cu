@@ -362,9 +362,12 @@ __device__ __forceinline__ void split_rows(const LinearParams& p, const Work& w,
   }
 }
 
-// kRaw: the copies bring bf16 rows, and the kernel takes them apart itself. (One
-// kernel for both: 7 rows, 129281 columns 64 us in place of 57.)
-template <bool kRaw>
+// What the loops of single threads go by is fixed when the kernel is compiled:
+// kRaw: the copies bring bf16 rows, and the kernel takes them apart itself (a
+//   switch in the loops: 7 rows, 129281 columns 64 us in place of 57);
+// kProducts of a K block, kHimg scale images of a product's columns (values read
+//   from the parameters: 1 row 7.9 us in place of 7.7, 4000 rows 110 in place of 102).
+template <bool kRaw, int kProducts, int kHimg>
 __global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
@@ -375,12 +378,10 @@ __global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __gri
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
   const int S = p.split;
   const Work w = work_of(p);
-  const int himg = p.cols > 128 ? 2 : 1;            // scale images of a product's columns
-  const int products = p.stacked ? 1 : p.parts;     // of a K block
 
   if (warp == 0) {
     if (lane < kMaxSlots) {
-      ptx::mbar_init(bar(bars->full[lane]), 2 + (kRaw ? 2 : products));  // the copies, the weights' images, each product's rows'
+      ptx::mbar_init(bar(bars->full[lane]), 2 + (kRaw ? 2 : kProducts));  // the copies, the weights' images, each product's rows'
       if (kRaw) ptx::mbar_init(bar(bars->raw[lane]), 1);
       ptx::mbar_init(bar(bars->empty[lane]), 1);
     } else if (lane >= 16 && lane < 18) {
@@ -421,11 +422,11 @@ __global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __gri
   if (warp >= kCodesW && warp < kCodesW + p.code_warps) {
     weight_codes(p, w, bars, smem, warp - kCodesW);
   } else if (warp >= kRowsX) {
-    const int who = warp - kRowsX, part = products > 1 ? who : 0;
-    const int turn = products > 1 ? 0 : who, turns = products > 1 ? 1 : p.turns;
+    const int who = warp - kRowsX, part = kProducts > 1 ? who : 0;
+    const int turn = kProducts > 1 ? 0 : who, turns = kProducts > 1 ? 1 : p.turns;
     if (kRaw)
       split_rows(p, w, bars, smem, who);
-    else if (himg == 1)
+    else if (kHimg == 1)
       row_codes<1>(p, w, bars, smem, part, turn, turns);
     else
       row_codes<2>(p, w, bars, smem, part, turn, turns);
@@ -480,9 +481,9 @@ __global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __gri
     if (elect_one()) {
       const uint32_t me = warp - kIssuer, tmem = bars->tmem;
       // A K block's scale columns in TMEM, by its slot: 4 of the weights, then 4
-      // himg of each product's rows. (The products take them from a column that
+      // kHimg of each product's rows. (The products take them from a column that
       // is a multiple of 4 only.)
-      const uint32_t sfx = 4 * himg, sf_slot = 4 + products * sfx;
+      const uint32_t sfx = 4 * kHimg, sf_slot = 4 + kProducts * sfx;
       const uint32_t sf0 = tmem + p.accs * p.issuers * p.cols;
       const uint32_t part_units = static_cast<uint32_t>(p.nt) * 8u;  // of 16 bytes, as descriptors count
       const uint32_t idesc = ptx::idesc_mxf8(p.cols, 0, ptx::kFmtE2M1), idesc_k = ptx::idesc_mxf8(0, 1, 0) - ptx::idesc_mxf8(0, 0, 0);
@@ -513,10 +514,12 @@ __global__ void __launch_bounds__(threads_of(kRaw), 1) linear_kernel(const __gri
           uint64_t b = b0 + slot.at * slot_b;
           const uint32_t sfa = sf0 + slot.at * sf_slot;
           ptx::tc_cp_32x128b_x4(sfa, img);
-          for (int h = 0; h < products; ++h, b += part_units) {
+#pragma unroll
+          for (int h = 0; h < kProducts; ++h, b += part_units) {
             const uint32_t sx = sfa + 4 + h * sfx;
-            for (int i = 0; i < himg; ++i)
-              ptx::tc_cp_32x128b_x4(sx + 4 * i, img + (1 + h * himg + i) * (kImg >> 4));
+#pragma unroll
+            for (int i = 0; i < kHimg; ++i)
+              ptx::tc_cp_32x128b_x4(sx + 4 * i, img + (1 + h * kHimg + i) * (kImg >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               ptx::tc_mma_mxf8(d, a + 2 * kk, b + 2 * kk, idesc + kk * idesc_k, sfa, sx, some);
@@ -747,6 +750,11 @@ bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q
 // last, 4 i + 1 blocks of K) that is 5 before and the one of the same issuer 10.
 int code_warps_of(int slots, int nk) { return slots >= 10 || (slots >= 6 && nk % 4 != 1) ? 2 : 1; }
 
+using Kernel = void (*)(LinearParams);
+constexpr Kernel kKernels[] = {linear_kernel<false, 1, 1>, linear_kernel<false, 1, 2>, linear_kernel<false, 2, 1>,
+                               linear_kernel<false, 2, 2>, linear_kernel<true, 1, 1>};
+constexpr int kRawKernel = 4;
+
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // How many clusters of each size the device holds at once (looked up once per device).
@@ -756,8 +764,8 @@ int max_clusters(int device, int split) {
   if (device < 0 || device >= kDevices) return 0;
   int n = known[device][split].load(std::memory_order_relaxed);
   if (n > 0) return n;
-  for (const void* f : {reinterpret_cast<const void*>(linear_kernel<false>), reinterpret_cast<const void*>(linear_kernel<true>)})
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess) return 0;
+  for (const Kernel k : kKernels)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split);
   cfg.blockDim = dim3(threads_of(true));
@@ -767,7 +775,7 @@ int max_clusters(int device, int split) {
   attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<true>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, kKernels[kRawKernel], &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -969,7 +977,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
   cfg.dynamicSmemBytes = p.off_bar + sizeof(Bars) + 1024;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shape.raw ? linear_kernel<true> : linear_kernel<false>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kKernels[shape.raw ? kRawKernel : 2 * (products - 1) + shape.himg - 1], p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
