@@ -29,6 +29,11 @@
 // other halves of its pairs) is a neighbour lane's chunk. Further CTAs of the
 // same grid turn the queries, spread evenly among these: one launch for q, k and
 // v, and the queries' stream fills the waits of the append's chains.
+// 40 query heads of 128 over 8: two prompts of 4100 tokens 41 us (214 MB, 5.2 TB/s;
+// 32 at the copy's rate, 48 with the queries' CTAs behind the append's), bound by
+// instructions (57 % of the cycles issue one at 17 warps an SM): every key/value
+// head's CTA makes the sines and cosines of its tokens. 48 sequences of one token
+// 4.5 us.
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"
@@ -113,8 +118,8 @@ struct RopeAppendParams : KvAppendParams {
 // The chunks that this thread loaded, turned (v[i]: token tid / kRowChunks + i *
 // kThreads / kRowChunks of the CTA's). One chunk's code, gone through in a loop
 // that moves the chunks on by one: unrolled over all of them it was 36 KB, and
-// took 52 us where this takes 42 (two prompts of 4100 tokens, 40 query heads of 128;
-// 6, 7 or 8 CTAs an SM by fewer registers: 42, 43, 46).
+// took 52 us where this takes 41 (two prompts of 4100 tokens, 40 query heads of 128;
+// 6, 7 or 8 CTAs an SM by fewer registers, 256 threads a CTA: 42, 43, 46, 42.5 to 49).
 template <int D, int kMax>
 __device__ __forceinline__ void turn_keys(const RopeAppendParams& p, uint4 (&v)[kMax], int count, int first_row,
                                           int first_pos) {
@@ -519,7 +524,7 @@ extern "C" int moe_rope_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seq
   p.ldq = ldq;
   p.ldqo = ldqo;
   p.q_heads = q_heads;
-  p.q_groups = rope::head_groups(p.tokens, q_heads, cache->head_dim);
+  p.q_groups = rope::head_groups(p.tokens, q_heads, cache->head_dim, true);
   p.slots = slots_of(p);
   const int64_t ctas = static_cast<int64_t>(p.slots) * cache->kv_heads * 2;
   const int64_t q_ctas =

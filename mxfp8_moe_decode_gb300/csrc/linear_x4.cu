@@ -12,6 +12,32 @@
 // Swap-AB: 128 weight rows are the MMA's M and up to 192 token rows its N, so
 // few tokens still fill the tensor cores' lanes, and the weights stream once
 // for up to 192 rows.
+//
+// A persistent CTA an SM, its warps by role around one ring of K blocks (128
+// columns): one thread copies weights (a 4-bit tensor copy that spreads the
+// codes as the tensor cores read them) and rows; warps gather the scale codes
+// from global memory into the images that tcgen05.cp takes; one or two threads
+// issue copies of scales and products; four warps take the sums out of TMEM.
+// Where a call has fewer tiles than SMs, a cluster shares a tile's K and sums
+// its parts in an exchange over distributed shared memory, in the order of the
+// ranks. choose_shape weighs tile heights and shares.
+//
+// What bounds it, and what it takes (calls back to back, weights from HBM):
+//  7 rows, 5120 -> 129281 columns (352 MB): the weights' stream, 56 us (6.3 TB/s)
+//  48 rows, 5120 -> 27648: 18.2 us, of which the stream is 11; the rest is the
+//    start, a CTA's last tile and the exchange
+//  1 row, 5120 -> 7168: 7.7 us. The stream is 2.9; 1.7 are a launch's, 1.1 the
+//    first codes and weights, 1.3 the exchange and the end, and a K block takes
+//    some 100 to 170 ns however few columns it has: one thread issues at most a
+//    block in 300, two half of that, four (a ring of 8 slots) no better
+//  4000 rows, 5120 -> 7168: 102 us, 2880 TFLOP/s; bf16 rows 196 (two products).
+//    The tensor cores work 64 % of the time (two accumulators of 192 columns
+//    fill TMEM, so one thread issues), shared memory 62 %
+// Slower: weights by plain loads through registers (7 rows above: 133 us) or by
+// cp.async and warps that spread the codes (91 to 107; shared memory's port);
+// pairs of CTAs that share the rows' copies by multicast (no change); tiles of 160
+// rows at most (4000 rows above, then 117 us: 141); the whole warp in the
+// issuing loop, fences with the writers, 4 blocks' scales at once (none faster).
 #include <cuda_fp8.h>
 
 #include <algorithm>

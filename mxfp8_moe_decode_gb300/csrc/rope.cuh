@@ -157,13 +157,17 @@ __device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int po
   }
 }
 
-// Threads that share a token's heads: all heads at once while the call is
-// small (its length is one thread's chain), else few, so that sines and cosines
-// serve several heads.
-inline int head_groups(int64_t tokens, int heads, int dim) {
+// Threads that share a token's heads. A thread's sines and cosines serve its
+// heads, but a small call lasts as long as one thread's chain. 40 heads of 128,
+// with 1, 4, 8 and 16 heads a thread (us):
+//   alone: 48 tokens (15000 items of 16 dims) 1.8, 2.0, 2.6, 3.6; 300: 2.9, 2.7, 3.5,
+//     5.3; 1000: 7.5, 5.4, 6.0, 7.2; 2000: 12.6, 8.6, 8.4, 9.6; 8000: 46.9, 26.5, 26.5, 27.4
+//   with the append, whose own chains are longer: 48 tokens 4.8, 4.6, 4.5, 5.3; 512:
+//     10.4, 9.1, 8.7, 8.5; 2000: 24.0, 16.9, 15.9, 14.7; 8200: 76.9, 45.3, 41.8, 40.9
+inline int head_groups(int64_t tokens, int heads, int dim, bool with_append) {
   const int64_t items = tokens * heads * (dim / 16);
-  if (items <= 152 * 2048) return heads;
-  return (heads + 7) / 8;
+  const int each = with_append ? (items <= 152 * 1024 ? 8 : 16) : items <= 152 * 256 ? 1 : items <= 152 * 3072 ? 4 : 8;
+  return (heads + each - 1) / each;
 }
 
 // Argument checks shared by the entry points.
