@@ -166,7 +166,7 @@ __device__ __forceinline__ void turn_heads(const Spec& r, const Heads& t, int po
 //     10.4, 9.1, 8.7, 8.5; 2000: 24.0, 16.9, 15.9, 14.7; 8200: 76.9, 45.3, 41.8, 40.9
 inline int head_groups(int64_t tokens, int heads, int dim, bool with_append) {
   const int64_t items = tokens * heads * (dim / 16);
-  const int each = with_append ? (items <= 152 * 1024 ? 8 : 16) : items <= 152 * 256 ? 1 : items <= 152 * 3072 ? 4 : 8;
+  const int each = with_append ? (items <= 152 * 1024 ? 8 : 16) : items <= 152 * 256 ? 1 : items <= 152 * 3000 ? 4 : 8;
   return (heads + each - 1) / each;
 }
 
