@@ -607,7 +607,8 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
  * Products are exact and sums fp32, with the one rounding of out; results do not
  * change from run to run (the order of a sum depends on M, N, K and the GPU). bf16 rows are multiplied as two MXFP8 rows, exact for
  * values down to 2^-14 of the largest of their 32 columns and off by at most 2^-21
- * of that largest below. A value of x that is not finite (a byte 0x7F or 0xFF, a
+ * of that largest (or 2^-137) below; a sum that passes fp32's range on the way is
+ * infinite or NaN. A value of x that is not finite (a byte 0x7F or 0xFF, a
  * code 255) makes its row of out NaN, and no other.
  *
  * workspace: for bf16 rows only (else null will do): device memory, 16-byte
@@ -616,8 +617,8 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
  * them, need workspaces of their own. One kernel on `stream` (bf16 rows: two); no
  * allocation, no synchronisation, capture safe. Errors: MOE_ERR_RANGE (M < 0 or >
  * 2^20, N < 0 or > 2^24), MOE_ERR_UNSUPPORTED (K not a multiple of 128 in [128,
- * 65536]), MOE_ERR_ARG (null, a stride below its row, a workspace that is too
- * small), MOE_ERR_ALIGN, MOE_ERR_CUDA. M = 0 or N = 0 enqueues nothing.
+ * 65536]), MOE_ERR_ARG (null, a stride below its row, out that is x, a
+ * workspace that is too small), MOE_ERR_ALIGN, MOE_ERR_CUDA. M = 0 or N = 0 enqueues nothing.
  */
 #define MOE_LINEAR_BF16 0
 #define MOE_LINEAR_MXFP8 1

@@ -917,7 +917,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   if (!aligned(x, 16) || !aligned(w, 32) || !aligned(w_codes, 4) || !aligned(out, 2) || !aligned(x_codes, 4) ||
       !aligned(status, 4) || !aligned(workspace, 16) || ldx % (x_codes ? 16 : 8))
     return MOE_ERR_ALIGN;
-  if (ldx < K || ldo < N) return MOE_ERR_ARG;
+  if (ldx < K || ldo < N || out == x) return MOE_ERR_ARG;
   const size_t need = moe_linear_x4_workspace_bytes(M, K, x_codes ? MOE_LINEAR_MXFP8 : MOE_LINEAR_BF16);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_ARG;
   int device = 0;

@@ -37,16 +37,24 @@ def quant_x4(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     the even code. For finite weights; K a multiple of 32."""
     if w.dim() != 2 or w.shape[1] % 32:
         raise ValueError(f"w must be [N, K] with K a multiple of 32, got {tuple(w.shape)}")
-    groups = w.double().view(w.shape[0], -1, 32)
-    m, e = torch.frexp(groups.abs().amax(-1) / 6.0)
-    code = (torch.where(m == 0.5, e - 1, e) + 127).clamp(0, 254) * (m > 0)  # a group of zeros: 0
-    v = groups * torch.exp2(127.0 - code.double())[..., None]
+    n, k = w.shape
+    packed = torch.empty(n, k // 2, dtype=torch.uint8, device=w.device)
+    codes = torch.empty(n, k // 32, dtype=torch.uint8, device=w.device)
     # the borders between E2M1's values; at .75, 1.75 and 3.5 the even code is the upper one
     border = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
     border = [math.nextafter(b, 0.0) if b in (0.75, 1.75, 3.5) else b for b in border]
-    nibble = torch.bucketize(v.abs().contiguous(), torch.tensor(border, dtype=torch.float64, device=w.device))
-    nibble = (nibble + 8 * torch.signbit(v)).to(torch.uint8).view(w.shape[0], -1, 2)
-    return nibble[..., 0] | (nibble[..., 1] << 4), code.to(torch.uint8)
+    border = torch.tensor(border, dtype=torch.float64, device=w.device)
+    step = max(1, (1 << 24) // max(k, 1))  # (rows at a time: what 64 bits take stays below a GB)
+    for lo in range(0, n, step):
+        groups = w[lo:lo + step].double().reshape(-1, k // 32, 32)
+        m, e = torch.frexp(groups.abs().amax(-1) / 6.0)
+        code = (torch.where(m == 0.5, e - 1, e) + 127).clamp(0, 254) * (m > 0)  # a group of zeros: 0
+        v = groups * torch.exp2(127.0 - code.double())[..., None]
+        nibble = torch.bucketize(v.abs().contiguous(), border)
+        nibble = (nibble + 8 * torch.signbit(v)).to(torch.uint8).view(-1, k // 2, 2)
+        packed[lo:lo + step] = nibble[..., 0] | (nibble[..., 1] << 4)
+        codes[lo:lo + step] = code.to(torch.uint8)
+    return packed, codes
 
 
 def dequant_x4(w: torch.Tensor, w_codes: torch.Tensor) -> torch.Tensor:

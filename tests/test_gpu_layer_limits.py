@@ -68,15 +68,18 @@ def _case(m, n, k, mx, seed=0):
 
 def _check(out, x, w, wc, xc, columns):
     """Some columns of out against fp64 (bounds as tests/test_gpu_layer.py: the sums, and bf16 rows off by 2^-21 of
-    their group's largest at most)."""
+    their group's largest at most). At the smallest numbers the formats' steps end: half of bf16's last step, 2^-133,
+    and of lo's, E4M3's 2^-9 under the code 0 (2^-127), for every value of x."""
     m, k = x.shape
     pick = torch.tensor(columns, device=DEV)
     rows = M.dequant_x4(w[pick], wc[pick]).double()
     v = x.double() if xc is None else (x.view(torch.float8_e4m3fn).double().view(m, -1, 32) *
                                        torch.exp2(xc.double() - 127)[..., None]).view(m, -1)
     slack = (k / 32 * 2.0 ** -23 + 2.0 ** -19) * v.abs() @ rows.abs().t()
+    slack += 2.0 ** -134
     if xc is None:
         slack += 2.0 ** -21 * v.abs().view(m, -1, 32).amax(-1).repeat_interleave(32, 1) @ rows.abs().t()
+        slack += 2.0 ** -137 * rows.abs().sum(1)
     exact = v @ rows.t()
     assert ((out[:, pick].double() - exact).abs() <= 2.0 ** -8 * exact.abs() + slack).all()
 
@@ -98,6 +101,35 @@ def test_linear_is_the_same_every_time(m, n, k, mx):
         wrong += (out.view(torch.int16) != want.view(torch.int16)).sum()
     assert wrong.item() == 0 and status.item() == 0
     _check(want, x, w, wc, xc, sorted({0, n // 2, n - 130, n - 1}))
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 150, 1024), (16, 600, 4096), (60, 300, 256),        # taken apart in the kernel
+                                   (24, 150, 65536), (60, 20000, 1024), (13, 40000, 1024),  # in front of it
+                                   (400, 3000, 1024), (150, 5000, 2048)])                   # as two products
+def test_linear_rows_taken_apart(m, n, k):
+    """bf16 rows on every way to the tensor cores: values over 2^-30 .. 2^30, groups of zeros, of the smallest and of
+    the largest numbers, and rows that are not finite, which touch no other."""
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+    w = torch.randint(0, 256, (n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    wc = torch.randint(115, 122, (n, k // 32), generator=g, device=DEV, dtype=torch.uint8)
+    x = torch.randn(m, k, generator=g, device=DEV) * torch.exp2(torch.randint(-30, 31, (m, k), generator=g, device=DEV).float())
+    x[:, 32:64] = 0.0
+    x[1] = 1e-39 * torch.randn(k, generator=g, device=DEV)                 # (subnormal in fp32 too)
+    x[m - 1] = x[m - 1].sign() * 1e38 * (1 + x[m - 1].abs() % 1)
+    x = x.bfloat16()
+    columns = sorted({0, 1, 100, 127, 128, n // 2, n - 20, n - 1})
+    out = M.linear_x4(x, w, wc)
+    seen = torch.isfinite(out[m - 1, columns]).all(0).item()               # (sums past fp32's range are infinite)
+    last = m if seen else m - 1
+    _check(out[:last], x[:last], w, wc, None, columns)
+    assert out[1, columns].double().abs().max() < 2.0 ** -90
+    bad = sorted({0, m // 2, m - 1})
+    x2 = x.clone()
+    x2[0, k - 1], x2[m // 2, 5], x2[m - 1, 40] = float("inf"), float("nan"), -float("inf")
+    out2 = M.linear_x4(x2, w, wc)
+    assert torch.isnan(out2[bad]).all()
+    rows = [i for i in range(m) if i not in bad]
+    assert torch.equal(out2[rows], out[rows])
 
 
 def test_linear_graphs_side_by_side():
@@ -179,6 +211,16 @@ def test_linear_rows_past_32_bits():
     wide = torch.empty(9, 300_000_000, dtype=torch.bfloat16, device=DEV)
     wide[:, :k] = x[:9]
     assert torch.equal(M.linear_x4(wide[:, :k], w, wc), M.linear_x4(x[:9].contiguous(), w, wc))
+
+
+@pytest.mark.parametrize("mx", [True, False])
+@pytest.mark.parametrize("m,n,k", [(1 << 20, 130, 128), (3, 1 << 24, 128)])
+def test_linear_at_its_limits(m, n, k, mx):
+    x, w, wc, xc = _case(m, n, k, mx)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = M.linear_x4(x, w, wc, x_codes=xc, status=status)
+    assert status.item() == 0
+    _check(out, x, w, wc, xc, sorted({0, 1, 129, n // 2, n - 1}))
 
 
 def test_norm_and_rope_rows_past_32_bits():

@@ -139,6 +139,7 @@ def test_linear_refusals(L):
     for name, by in (("x", 8), ("w", 16), ("wc", 2), ("out", 1), ("xc", 2), ("ws", 8), ("status", 2)):
         assert call(**{name: P[9] + by}) == MOE_ERR_ALIGN, name
     assert call(ldx=240) == MOE_ERR_ARG and call(ldo=99) == MOE_ERR_ARG
+    assert call(out=P[0]) == MOE_ERR_ARG  # in place
     assert call(ldx=264) == MOE_ERR_ALIGN           # bytes: 16 at a time
     assert call(xc=None, ldx=260) == MOE_ERR_ALIGN  # bf16: 8 values at a time
     # bf16 rows need a workspace, MXFP8 rows none

@@ -119,3 +119,13 @@ def test_quant_x4_takes_the_smallest_scale():
     assert packed.shape == (3, 32)
     with pytest.raises(ValueError):
         quant_x4(w[:, :40])
+
+
+def test_quant_x4_in_parts():
+    """Rows that are taken a few at a time come out as each by itself, strided ones and none at all too."""
+    k = 1 << 23
+    w = torch.randn(5, 64).repeat(1, k // 64)
+    packed, c = quant_x4(w)
+    one, one_c = quant_x4(w[:, :64].t().contiguous().t())
+    assert torch.equal(packed.view(5, -1, 32)[:, 7], one) and torch.equal(c.view(5, -1, 2)[:, -1], one_c)
+    assert quant_x4(w[:0, :64])[0].shape == (0, 32)
