@@ -25,15 +25,16 @@
 //
 // With rotary positions (kRope, rope.cuh) the keys' CTAs turn what they loaded
 // and round it to bf16 before anything looks at it, so the cache gets the bytes
-// it would get from keys that another kernel had turned. A chunk's partner (the
-// other halves of its pairs) is a neighbour lane's chunk. Further CTAs of the
-// same grid turn the queries, spread evenly among these: one launch for q, k and
-// v, and the queries' stream fills the waits of the append's chains.
-// 40 query heads of 128 over 8: two prompts of 4100 tokens 41 us (214 MB, 5.2 TB/s;
-// 32 at the copy's rate, 48 with the queries' CTAs behind the append's), bound by
-// instructions (57 % of the cycles issue one at 17 warps an SM): every key/value
-// head's CTA makes the sines and cosines of its tokens. 48 sequences of one token
-// 4.5 us.
+// it would get from keys that another kernel had turned. A thread loads both
+// values of its pairs (chunks that neighbour lanes exchanged: 40.9 us in place
+// of 38.5 below). Further CTAs of the same grid turn the queries, spread evenly
+// among these: one launch for q, k and v, and the queries' stream fills the waits
+// of the append's chains.
+// 40 query heads of 128 over 8: two prompts of 4100 tokens 38.5 us (214 MB, 5.6
+// TB/s; 32 at the copy's rate, 48 with the queries' CTAs behind the append's),
+// bound by instructions: every key/value head's CTA makes the sines and cosines
+// of its tokens. 48 sequences of one token 4.5 us. By fewer registers 6 or 7 CTAs
+// an SM in place of 5: 38.5 and 38.9, 4 x 128 tokens 9.0 in place of 8.5.
 #include "internal.cuh"
 #include "kv_x8.cuh"
 #include "mx.cuh"
@@ -115,65 +116,41 @@ struct RopeAppendParams : KvAppendParams {
   unsigned q_share;         // the queries' part of the CTAs, in units of 2^-32, rounded up
 };
 
-// The chunks that this thread loaded, turned (v[i]: token tid / kRowChunks + i *
-// kThreads / kRowChunks of the CTA's). One chunk's code, gone through in a loop
-// that moves the chunks on by one: unrolled over all of them it was 36 KB, and
-// took 52 us where this takes 41 (two prompts of 4100 tokens, 40 query heads of 128;
-// 6, 7 or 8 CTAs an SM by fewer registers, 256 threads a CTA: 42, 43, 46, 42.5 to 49).
+// The keys that this thread loaded, turned: item j's two chunks of the tokens
+// tid / kItems, + kThreads / kItems, ... of the CTA's (rope::item_chunks: both
+// values of its pairs are here). One item's code, gone through in a loop that
+// moves the chunks on by two (all of a thread's chunks unrolled, in an earlier
+// form: 36 KB of code, 52 us where the loop took 42).
 template <int D, int kMax>
 __device__ __forceinline__ void turn_keys(const RopeAppendParams& p, uint4 (&v)[kMax], int count, int first_row,
                                           int first_pos) {
-  constexpr int kRowChunks = D / 8;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int chunks = p.spec.rot >> 3, half = chunks >> 1;
-  const int at = tid % kRowChunks - (p.spec.first >> 3);  // among the rotated chunks
-  const bool turns = at >= 0 && at < chunks, low = at < half;
-  // Its pairs: 4 of neighbours, or 8 with the chunk `half` further or back. Of
-  // those 8 each of the two makes the sines and cosines of 4.
-  const int pair0 = p.spec.interleaved ? 4 * at : low ? 8 * at : 8 * (at - half) + 4;
-  const int partner = !turns || p.spec.interleaved ? lane : low ? lane + half : lane - half;
-  uint64_t f[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = turns ? __ldg(p.spec.freqs + pair0 + j) : 0;
-  const auto from = [partner](unsigned long long x) { return __shfl_sync(0xffffffffu, x, partner); };
-  const auto turn_one = [&](uint4& x, int i) {
-    const int row = min((tid + i * kThreads) / kRowChunks, count - 1);
+  constexpr int kItems = D / 16, kTokens = kThreads / kItems;
+  const int j = threadIdx.x % kItems;
+  if (16 * j >= p.spec.rot) return;  // (the item's dims do not turn)
+  const ulonglong2* f = reinterpret_cast<const ulonglong2*>(p.spec.freqs + rope::kPairs * j);
+  const auto turn_one = [&](uint4& a, uint4& b, int row) {
     const int pos = p.positions ? __ldg(p.positions + first_row + row) : first_pos + row;
-    Pair c[2], s[2];
+    Pair c[4], s[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) rope::turn(pos, f[2 * j], f[2 * j + 1], p.spec.scale, c[j], s[j]);
+    for (int i = 0; i < 4; ++i) {
+      const ulonglong2 g = __ldg(f + i);
+      rope::turn(pos, g.x, g.y, p.spec.scale, c[i], s[i]);
+    }
     if (p.spec.interleaved) {
-      if (turns) rope::turn_neighbours(x, c, s);
-      return;
+      rope::turn_neighbours(a, c, s);
+      rope::turn_neighbours(b, c + 2, s + 2);
+    } else {
+      rope::turn_halves(a, b, c, s);
     }
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, x.x, partner);
-    o.y = __shfl_sync(0xffffffffu, x.y, partner);
-    o.z = __shfl_sync(0xffffffffu, x.z, partner);
-    o.w = __shfl_sync(0xffffffffu, x.w, partner);
-    Pair oc[2], os[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      oc[j].v = from(c[j].v);
-      os[j].v = from(s[j].v);
-    }
-    const Pair ac[4] = {low ? c[0] : oc[0], low ? c[1] : oc[1], low ? oc[0] : c[0], low ? oc[1] : c[1]};
-    const Pair as[4] = {low ? s[0] : os[0], low ? s[1] : os[1], low ? os[0] : s[0], low ? os[1] : s[1]};
-    uint4 a = low ? x : o, b = low ? o : x;
-    rope::turn_halves(a, b, ac, as);
-    if (turns) x = low ? a : b;
   };
-  if (count * kRowChunks <= kThreads) {  // (a decode step's)
-    turn_one(v[0], 0);
-    return;
-  }
 #pragma unroll 1
-  for (int i = 0; i < kMax; ++i) {
-    uint4 x = v[0];
-    if ((tid & ~31) + i * kThreads < count * kRowChunks) turn_one(x, i);  // (uniform in the warp)
+  for (int i = 0, row = threadIdx.x / kItems; i < kMax / 2; ++i, row += kTokens) {
+    uint4 x = v[0], y = v[1];
+    if (row < count) turn_one(x, y, row);
 #pragma unroll
-    for (int j = 0; j + 1 < kMax; ++j) v[j] = v[j + 1];
-    v[kMax - 1] = x;
+    for (int k = 0; k + 2 < kMax; ++k) v[k] = v[k + 2];
+    v[kMax - 2] = x;
+    v[kMax - 1] = y;
   }
 }
 
@@ -306,15 +283,31 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Params p) {
 
   // the values are on their way while the page is looked up
   uint4 v[kMax];
-#pragma unroll
-  for (int i = 0; i < kMax; ++i) {
-    const int c = tid + i * kThreads;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (c < count * kRowChunks)
-      v[i] = __ldcs(reinterpret_cast<const uint4*>(src + (c / kRowChunks) * ld) + c % kRowChunks);
-  }
+  // keys that are to be turned: chunk i is the first or second of an item's of the token `key_token(i)`
+  constexpr int kItems = D / 16;
+  int chunk[2] = {0, 0};
+  const auto key_token = [tid](int i) { return tid / kItems + (i >> 1) * (kThreads / kItems); };
+  const bool turned = kRope && kv == 0;
   if constexpr (kRope) {
-    if (kv == 0) turn_keys<D>(p, v, count, c0 + (t0 - start), t0);
+    if (turned) {
+      rope::item_chunks(p.spec, tid % kItems, chunk[0], chunk[1]);
+#pragma unroll
+      for (int i = 0; i < kMax; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (key_token(i) < count)
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(src + key_token(i) * ld) + chunk[i & 1]);
+      }
+      turn_keys<D>(p, v, count, c0 + (t0 - start), t0);
+    }
+  }
+  if (!turned) {
+#pragma unroll
+    for (int i = 0; i < kMax; ++i) {
+      const int c = tid + i * kThreads;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (c < count * kRowChunks)
+        v[i] = __ldcs(reinterpret_cast<const uint4*>(src + (c / kRowChunks) * ld) + c % kRowChunks);
+    }
   }
   int page = -1;
   if (page_index < p.max_pages)
@@ -354,6 +347,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Params p) {
   }
   if (tid == 0) p.codes[owner] = static_cast<uint8_t>(code);
   const __nv_bfloat162 mul = __float2bfloat162_rn(mx_mul(code));
+  if (turned) {
+#pragma unroll
+    for (int i = 0; i < kMax; ++i)
+      if (key_token(i) < count)
+        *reinterpret_cast<uint2*>(img + key_byte<D>(off + key_token(i), chunk[i & 1] * 8)) = quant8(v[i], mul);
+    return;
+  }
   if (kv == 0) {
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {
