@@ -17,7 +17,7 @@
 // once, and the two sums cost two exchanges of four floats.
 // 12000 rows of 5120: with a gate per row 91 us (556 MB, 6.1 TB/s, 91 % of a copy's
 // rate), without 73, with normed 88. Arithmetic is in fp32 pairs, and what scales a
-// row is one factor (before: 104 us, bound by instructions). 48 rows 4.7 us: a
+// row is one factor (before: 104 us, bound by instructions). 48 rows 3.3 us: a
 // launch and one row's chain of loads, two exchanges and stores. Six CTAs an SM
 // where a thread has 4 or 5 octets: 93.4 us without (79 registers hold the rows of
 // 5120; of wider ones they would not).
@@ -46,9 +46,10 @@ struct NormAddNormParams {
   float eps, res_scale, block_scale;
 };
 
-// kOct octets a thread (H <= 1024 kOct)
-template <int kOct>
-__global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm_add_norm_kernel(const NormAddNormParams p) {
+// kOct octets a thread (H <= 1024 kOct); kFew: the weights are loaded with the
+// rows, before the sums that they wait for otherwise (launch says when)
+template <int kOct, bool kFew>
+__global__ void __launch_bounds__(kThreads, !kFew && (kOct == 4 || kOct == 5) ? 6 : 1) norm_add_norm_kernel(const NormAddNormParams p) {
   const size_t t = blockIdx.x;
   const int H = p.H;
   const int noct = H >> 3;
@@ -71,6 +72,15 @@ __global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm
     b[i] = in ? __ldcs(xr + o) : zero;
     s[i] = in ? __ldcs(rr + o) : zero;
     g[i] = in && gated ? (p.ldg ? __ldcs(gr + o) : __ldg(gr + o)) : zero;
+  }
+  uint4 pw[kFew ? kOct : 1], nw[kFew ? kOct : 1];
+  if (kFew) {
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const int o = tid + i * kThreads;
+      pw[i] = o < noct && post ? __ldg(pr + o) : zero;
+      nw[i] = o < noct ? __ldg(wr + o) : zero;
+    }
   }
   float rx = p.block_scale;
   if (post) {
@@ -96,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm
   for (int i = 0; i < kOct; ++i) {
     const int o = tid + i * kThreads;
     if (o < noct) {
-      const uint4 m = post ? __ldg(pr + o) : zero;
+      const uint4 m = kFew ? pw[kFew ? i : 0] : post ? __ldg(pr + o) : zero;
       const uint32_t xs[4] = {b[i].x, b[i].y, b[i].z, b[i].w}, ms[4] = {m.x, m.y, m.z, m.w},
                      gs[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
       uint32_t r[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
@@ -127,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm
     const int o = tid + i * kThreads;
     if (i * kThreads >= noct) break;  // uniform across the CTA
     const bool in = o < noct;
-    const uint4 w = in ? __ldg(wr + o) : zero;
+    const uint4 w = kFew ? nw[kFew ? i : 0] : in ? __ldg(wr + o) : zero;
     const uint32_t vs[4] = {s[i].x, s[i].y, s[i].z, s[i].w}, ws[4] = {w.x, w.y, w.z, w.w};
     Pair y[4];
     float amax = 0.0f;
@@ -166,9 +176,13 @@ __global__ void __launch_bounds__(kThreads, kOct == 4 || kOct == 5 ? 6 : 1) norm
   }
 }
 
+// Rows for which the SMs have room at once: a call lasts one row's chain (5120
+// columns: 48 rows 3.3 us in place of 4.7, 600 rows 6.9 in place of 8.6). Of more,
+// more CTAs an SM hide it, whose registers hold no weights (600 rows of 8192: 13.9
+// us, with the weights first 14.7).
 template <int kOct>
 cudaError_t launch(const NormAddNormParams& p, int M, cudaStream_t s) {
-  return launch_pdl(norm_add_norm_kernel<kOct>, dim3(M), dim3(kThreads), 0, s, p);
+  return launch_pdl(M <= 152 * (kOct > 5 ? 2 : 4) ? norm_add_norm_kernel<kOct, true> : norm_add_norm_kernel<kOct, false>, dim3(M), dim3(kThreads), 0, s, p);
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
