@@ -71,7 +71,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSmemMax = 227 * 1024;
 
 struct LinearParams {
-  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]
+  CUtensorMap tm_x;      // the rows' parts: [K / 128][part][M][128]; bf16 rows (kRaw): [K / 64][M][128 bytes]
   CUtensorMap tm_w;      // the weights: [K / 128][N][128 of 4 bits], a box one K block of a tile
   const uint8_t* wc;     // [N][K / 32]
   const uint8_t* xc[2];  // [M][K / 32]
