@@ -58,12 +58,13 @@ def quant_x4(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
 
 
 def dequant_x4(w: torch.Tensor, w_codes: torch.Tensor) -> torch.Tensor:
-    """The values that MXFP4 rows stand for, fp32 [N, K] (for tests and
-    inspection: torch operations, any device)."""
+    """The values that MXFP4 rows stand for, fp32 [N, K], NaN under the code 255
+    (for tests and inspection: torch operations, any device)."""
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=w.device)
     table = torch.cat((table, -table))
     v = torch.stack((table[(w & 15).long()], table[(w >> 4).long()]), -1).view(w.shape[0], -1, 32)
-    return (v.double() * torch.exp2(w_codes.double() - 127)[..., None]).float().view(w.shape[0], -1)
+    scale = torch.exp2(w_codes.double() - 127).masked_fill(w_codes == 255, math.nan)
+    return (v.double() * scale[..., None]).float().view(w.shape[0], -1)
 
 
 def linear_x4_workspace_bytes(rows: int, cols: int, mxfp8: bool) -> int:

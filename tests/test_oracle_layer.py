@@ -129,3 +129,18 @@ def test_quant_x4_in_parts():
     one, one_c = quant_x4(w[:, :64].t().contiguous().t())
     assert torch.equal(packed.view(5, -1, 32)[:, 7], one) and torch.equal(c.view(5, -1, 2)[:, -1], one_c)
     assert quant_x4(w[:0, :64])[0].shape == (0, 32)
+
+
+@pytest.mark.parametrize("code", [0, 1, 127, 254, 255])
+def test_dequant_x4_takes_every_code(code):
+    """The code 255 makes every value of its group NaN, zeros among them; all others are powers of two."""
+    w = torch.arange(16, dtype=torch.uint8)[None]  # (low nibbles 0 .. 15, high nibbles 0)
+    w = torch.cat((w, w), 1)
+    got = dequant_x4(w, torch.tensor([[code, 127]], dtype=torch.uint8))
+    values = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0])
+    plain = torch.stack((values, torch.zeros(16)), -1).view(1, 32)
+    assert torch.equal(got[:, 32:], plain)
+    if code == 255:
+        assert torch.isnan(got[:, :32]).all()
+    else:  # (2^127 times 4 and 6 lie beyond fp32)
+        assert torch.equal(got[:, :32], (plain.double() * 2.0 ** (code - 127)).float())
