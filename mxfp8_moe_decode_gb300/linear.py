@@ -62,9 +62,9 @@ def dequant_x4(w: torch.Tensor, w_codes: torch.Tensor) -> torch.Tensor:
     (for tests and inspection: torch operations, any device)."""
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=w.device)
     table = torch.cat((table, -table))
-    v = torch.stack((table[(w & 15).long()], table[(w >> 4).long()]), -1).view(w.shape[0], -1, 32)
+    v = torch.stack((table[(w & 15).long()], table[(w >> 4).long()]), -1).view(*w_codes.shape, 32)
     scale = torch.exp2(w_codes.double() - 127).masked_fill(w_codes == 255, math.nan)
-    return (v.double() * scale[..., None]).float().view(w.shape[0], -1)
+    return (v.double() * scale[..., None]).float().flatten(1)
 
 
 def linear_x4_workspace_bytes(rows: int, cols: int, mxfp8: bool) -> int:

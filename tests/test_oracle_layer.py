@@ -144,3 +144,9 @@ def test_dequant_x4_takes_every_code(code):
         assert torch.isnan(got[:, :32]).all()
     else:  # (2^127 times 4 and 6 lie beyond fp32)
         assert torch.equal(got[:, :32], (plain.double() * 2.0 ** (code - 127)).float())
+
+
+def test_dequant_x4_of_no_rows():
+    """What quant_x4 makes of no rows goes back as it came."""
+    assert dequant_x4(*quant_x4(torch.zeros(0, 64))).shape == (0, 64)
+    assert dequant_x4(*quant_x4(torch.ones(2, 64))).equal(torch.ones(2, 64))
