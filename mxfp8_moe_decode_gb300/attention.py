@@ -90,8 +90,10 @@ def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: in
     divided by it, or with ``trained`` (the length the model was trained on) by
     parts: pairs that turn ``fast`` times or more within that length keep their
     frequency, those that turn ``slow`` times or less are divided, the pairs
-    between them are mixed linearly by their number. (The factor of cos and sin
-    that goes with it is :func:`rope`'s ``scale``.)
+    between them are mixed linearly by their number. (Given frequencies must fall
+    for that, and are positive; where the two borders lie among them goes by the
+    line of their logarithms. The factor of cos and sin that goes with it is
+    :func:`rope`'s ``scale``.)
     """
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and positive, got {rot}")
@@ -104,8 +106,15 @@ def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: in
     if trained is None:
         f = [v / factor for v in f]
     else:
+        if inv_freq is not None and (n < 2 or f[-1] <= 0 or any(a <= b for a, b in zip(f, f[1:]))):
+            raise ValueError("inv_freq must be positive and fall from pair to pair to be scaled by parts")
+
         def pair(turns):  # the pair (not whole) that turns so often within the trained length
-            return n * math.log(trained / (turns * 2 * math.pi)) / math.log(base)
+            if inv_freq is None:
+                return n * math.log(trained / (turns * 2 * math.pi)) / math.log(base)
+            border = turns * 2 * math.pi / trained
+            i = min(max(sum(v > border for v in f) - 1, 0), n - 2)  # (beyond the ends the last two's line goes on)
+            return i + math.log(f[i] / border) / math.log(f[i] / f[i + 1])
 
         low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
         for i in range(n):

@@ -150,3 +150,35 @@ def test_dequant_x4_of_no_rows():
     """What quant_x4 makes of no rows goes back as it came."""
     assert dequant_x4(*quant_x4(torch.zeros(0, 64))).shape == (0, 64)
     assert dequant_x4(*quant_x4(torch.ones(2, 64))).equal(torch.ones(2, 64))
+
+
+@pytest.mark.parametrize("base", [100.0, 10000.0, 500000.0, 1e7])
+@pytest.mark.parametrize("rot,trained", [(16, 500), (128, 8192), (128, 40), (256, 1000000)])
+def test_rope_freqs_by_parts_of_given_frequencies(rot, trained, base):
+    """Frequencies that are given are kept, mixed and divided by what they turn themselves: a base's own series gives
+    that base's numbers (the borders of fast and slow pairs also beyond the first and the last pair)."""
+    kw = dict(rot=rot, factor=8.0, trained=trained, device="cpu")
+    want = unsigned(rope_freqs(base=base, **kw))
+    got = unsigned(rope_freqs(inv_freq=[base ** (-2.0 * i / rot) for i in range(rot // 2)], **kw))
+    # (the line between two borders that lie at least a pair apart moves with their last bits only)
+    assert all(abs(a - b) <= 2.0 ** -40 * b + 1 for a, b in zip(got, want))
+
+
+def test_rope_freqs_by_parts_of_an_uneven_series():
+    """By hand: turns within the trained length 64, 32, 8, 4, 1, 1/4."""
+    trained, turns = 1000, [64.0, 32.0, 8.0, 4.0, 1.0, 0.25]
+    f = [t * 2 * math.pi / trained for t in turns]
+    got = unsigned(rope_freqs(12, inv_freq=f, factor=4.0, trained=trained, fast=30.0, slow=1.5, device="cpu"))
+    # 30 turns lie behind pair 1, 1.5 turns before pair 4: a line from pair 1 to pair 4
+    for g, t, mix in zip(got, turns, [0.0, 0.0, 1 / 3, 2 / 3, 1.0, 1.0]):
+        want = t / trained * (1 - mix + mix / 4.0) * 2.0 ** 64
+        assert abs(g - want) <= 2.0 ** -45 * want + 1
+
+
+@pytest.mark.parametrize("f", [[1.0, 1.0, 0.5, 0.1], [0.1, 0.5, 1.0, 2.0], [1.0, 0.5, 0.0, -1.0], [1.0, 0.1, 0.2, 0.01]])
+def test_rope_freqs_by_parts_refuses_frequencies_that_do_not_fall(f):
+    with pytest.raises(ValueError):
+        rope_freqs(8, inv_freq=f, factor=2.0, trained=1000, device="cpu")
+    assert rope_freqs(8, inv_freq=f, factor=2.0, device="cpu").shape == (4,)
+    with pytest.raises(ValueError):  # (one pair has no neighbour)
+        rope_freqs(2, inv_freq=[1.0], factor=2.0, trained=1000, device="cpu")
