@@ -98,6 +98,8 @@ def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: in
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and positive, got {rot}")
     n = rot // 2
+    if inv_freq is None and not 0 < base < math.inf:
+        raise ValueError(f"base must be finite and positive, got {base}")
     f = [base ** (-2.0 * i / rot) for i in range(n)] if inv_freq is None else [float(v) for v in inv_freq]
     if len(f) != n:
         raise ValueError(f"inv_freq must have {n} values, got {len(f)}")
@@ -106,6 +108,10 @@ def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: in
     if trained is None:
         f = [v / factor for v in f]
     else:
+        if not 0 < trained < math.inf or not 0 < slow <= fast < math.inf:
+            raise ValueError("trained must be positive, and 0 < slow <= fast")
+        if inv_freq is None and base <= 1:
+            raise ValueError(f"base must be above 1 to scale by parts, got {base}")
         if inv_freq is not None and (n < 2 or f[-1] <= 0 or any(a <= b for a, b in zip(f, f[1:]))):
             raise ValueError("inv_freq must be positive and fall from pair to pair to be scaled by parts")
 
@@ -120,6 +126,8 @@ def rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: in
         for i in range(n):
             keep = 1.0 - min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0)
             f[i] *= keep + (1.0 - keep) / factor
+    if not all(map(math.isfinite, f)):
+        raise ValueError("frequencies divided by the factor must be finite")
     turns = [round(math.ldexp(v / (2 * math.pi), 64)) % (1 << 64) for v in f]
     return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
 

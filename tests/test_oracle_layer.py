@@ -182,3 +182,13 @@ def test_rope_freqs_by_parts_refuses_frequencies_that_do_not_fall(f):
     assert rope_freqs(8, inv_freq=f, factor=2.0, device="cpu").shape == (4,)
     with pytest.raises(ValueError):  # (one pair has no neighbour)
         rope_freqs(2, inv_freq=[1.0], factor=2.0, trained=1000, device="cpu")
+
+
+@pytest.mark.parametrize("kw", [dict(base=-2.0), dict(base=0.0), dict(base=float("nan")), dict(base=float("inf")),
+                                dict(base=1.0, trained=100), dict(base=0.5, trained=100), dict(trained=0), dict(trained=-5),
+                                dict(trained=float("nan")), dict(trained=100, slow=0.0), dict(trained=100, slow=-1.0),
+                                dict(trained=100, fast=1.0, slow=32.0), dict(trained=100, fast=float("nan")),
+                                dict(trained=100, fast=float("inf")), dict(inv_freq=[1e300] * 4, factor=1e-300)])
+def test_rope_freqs_refuses_what_no_formula_covers(kw):
+    with pytest.raises(ValueError):
+        rope_freqs(8, device="cpu", **{"factor": 2.0, **kw})
