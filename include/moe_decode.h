@@ -628,6 +628,27 @@ int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes, int M, con
                   size_t workspace_bytes, int32_t* status, void* stream);
 size_t moe_linear_x4_workspace_bytes(int M, int K, int x_format);
 
+/*
+ * How moe_linear_x4 lays a call out on the current device (for tests and
+ * inspection; nothing is enqueued). M and N at least 1, else as moe_linear_x4.
+ */
+typedef struct moe_linear_shape {
+  int tile_rows;     /* token rows of a tile (128 weight rows each) */
+  int tiles;
+  int split;         /* CTAs (a cluster) that share a tile's K */
+  int clusters;      /* clusters of that size that the device holds */
+  int products;      /* products of a K block: 2 for bf16 rows as hi and lo apart */
+  int images;        /* scale images of a product's rows */
+  int stacked;       /* hi and lo are columns of one product */
+  int inside;        /* bf16 rows are taken apart in the kernel; the workspace is not touched */
+  int over;          /* the exchange buffer of a cluster lies over the ring */
+  int issuers;
+  int slots;         /* K blocks that the ring holds */
+  int weight_warps;  /* warps that make the weights' scale images */
+  int row_warps;     /* warps that take the rows' K blocks in turn */
+} moe_linear_shape;
+int moe_linear_x4_shape(int M, int N, int K, int x_format, moe_linear_shape* shape);
+
 #ifdef __cplusplus
 }
 #endif

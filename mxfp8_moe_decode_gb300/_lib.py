@@ -73,6 +73,12 @@ class RopeSpec(ctypes.Structure):
 LINEAR_BF16, LINEAR_MXFP8 = 0, 1
 LINEAR_STATUS_TIMEOUT = 1
 
+
+class LinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("tile_rows", "tiles", "split", "clusters", "products", "images", "stacked",
+                                            "inside", "over", "issuers", "slots", "weight_warps", "row_warps")]
+
+
 _LIB = None
 
 
@@ -131,6 +137,8 @@ def lib() -> ctypes.CDLL:
     L.moe_linear_x4.restype = ip
     L.moe_linear_x4_workspace_bytes.argtypes = [ip, ip, ip]
     L.moe_linear_x4_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_linear_x4_shape.argtypes = [ip, ip, ip, ip, ctypes.POINTER(LinearShape)]
+    L.moe_linear_x4_shape.restype = ip
     L.moe_kv_append_x8.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), vp, i64, vp,
                                    i64, vp, vp]
     L.moe_kv_append_x8.restype = ip

@@ -894,6 +894,15 @@ bool choose_shape(int M, int N, int K, int parts, int device, Shape& best) {
   return any;
 }
 
+int weight_code_warps(const Shape& s, int K) { return code_warps_of(s.slots, K / 128); }
+
+// Warps that take the blocks' rows' codes (s.raw: pairs of warps, their bf16 rows)
+// in turn; of two products, one each. Four where a CTA has whole tiles to stream:
+// 129281 columns of 5120, 7 rows 56 us, with two 59.
+int row_turns(const Shape& s) {
+  return s.slots % 2 ? 1 : (s.slots >= 6 && s.split == 1) || (s.raw && s.slots >= 4) ? 4 : 2;
+}
+
 // One part's codes in the workspace.
 size_t split_codes(int M, int K) { return (static_cast<size_t>(M) * K / 32 + 15) / 16 * 16; }
 
@@ -904,6 +913,23 @@ extern "C" size_t moe_linear_x4_workspace_bytes(int M, int K, int x_format) {
   return x_format == MOE_LINEAR_BF16 && M > 0 && K > 0
              ? 2 * (static_cast<size_t>(M) * K + moe::split_codes(M, K))
              : 0;
+}
+
+extern "C" int moe_linear_x4_shape(int M, int N, int K, int x_format, moe_linear_shape* shape) {
+  using namespace moe;
+  if (M < 1 || M > (1 << 20) || N < 1 || N > (1 << 24)) return MOE_ERR_RANGE;
+  if (K < 128 || K % 128 || K > (1 << 16)) return MOE_ERR_UNSUPPORTED;
+  if (!shape || (x_format != MOE_LINEAR_BF16 && x_format != MOE_LINEAR_MXFP8)) return MOE_ERR_ARG;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  Shape s;
+  if (!choose_shape(M, N, K, x_format == MOE_LINEAR_BF16 ? 2 : 1, device, s)) return MOE_ERR_CUDA;
+  *shape = {s.nt,       static_cast<int>(s.tasks), s.split, s.clusters, s.products, s.himg, s.stacked, s.raw, s.over,
+            s.issuers,  s.slots,                   weight_code_warps(s, K),         s.products > 1 ? 1 : row_turns(s)};
+  return MOE_OK;
 }
 
 extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes, int M, const uint8_t* w,
@@ -951,10 +977,8 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.split = split;
   p.slot_b = p.parts * p.nt * 128u;
   p.slot_img = (1 + products * shape.himg) * kImg;
-  p.code_warps = code_warps_of(p.slots, K / 128);
-  // (four warps where a CTA has whole tiles to stream: 129281 columns of 5120, 7 rows
-  // 56 us, with two 59)
-  p.turns = p.slots % 2 ? 1 : (p.slots >= 6 && split == 1) || (shape.raw && p.slots >= 4) ? 4 : 2;
+  p.code_warps = weight_code_warps(shape, K);
+  p.turns = row_turns(shape);
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
   // (a ring has 3 slots at least, more than the 96 KB that an exchange buffer over it takes)

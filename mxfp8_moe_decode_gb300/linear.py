@@ -70,3 +70,13 @@ def dequant_x4(w: torch.Tensor, w_codes: torch.Tensor) -> torch.Tensor:
 def linear_x4_workspace_bytes(rows: int, cols: int, mxfp8: bool) -> int:
     """Bytes of workspace that :func:`linear_x4` needs for x [rows, cols]."""
     return _lib.lib().moe_linear_x4_workspace_bytes(rows, cols, _lib.LINEAR_MXFP8 if mxfp8 else _lib.LINEAR_BF16)
+
+
+def linear_x4_shape(rows: int, cols: int, out: int, mxfp8: bool, device="cuda") -> dict:
+    """How :func:`linear_x4` lays out x [rows, cols] onto ``out`` columns on a
+    device (``moe_linear_shape``; for tests and inspection)."""
+    shape = _lib.LinearShape()
+    with torch.cuda.device(device):
+        rc = _lib.lib().moe_linear_x4_shape(rows, out, cols, _lib.LINEAR_MXFP8 if mxfp8 else _lib.LINEAR_BF16, shape)
+    _result(rc, "moe_linear_x4_shape")
+    return {name: getattr(shape, name) for name, _ in shape._fields_}

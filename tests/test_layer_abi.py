@@ -151,6 +151,23 @@ def test_linear_refusals(L):
     assert M.linear_x4_workspace_bytes(4, 256, mxfp8=False) == need
 
 
+def test_linear_shape_refusals(L):
+    def call(m=4, n=100, k=256, form=_lib.LINEAR_BF16, shape=None):
+        return L.moe_linear_x4_shape(m, n, k, form, shape or _lib.LinearShape())
+
+    for v in (0, -1, (1 << 20) + 1):
+        assert call(m=v) == MOE_ERR_RANGE
+    for v in (0, -1, (1 << 24) + 1):
+        assert call(n=v) == MOE_ERR_RANGE
+    for v in (0, 64, 192, -128, (1 << 16) + 128):
+        assert call(k=v) == MOE_ERR_UNSUPPORTED
+    assert call(form=2) == MOE_ERR_ARG and call(form=-1) == MOE_ERR_ARG
+    assert L.moe_linear_x4_shape(4, 100, 256, 0, None) == MOE_ERR_ARG
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe_decode.h")).read()
+    body = re.search(r"typedef struct moe_linear_shape \{(.*?)\} moe_linear_shape;", src, re.S)[1]
+    assert re.findall(r"int (\w+);", body) == [name for name, _ in _lib.LinearShape._fields_]
+
+
 def test_bindings_refuse_host_tensors_and_shapes():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
