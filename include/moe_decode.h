@@ -606,7 +606,7 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
  * The weights are read as they are: nothing is laid out before, nothing is kept.
  * Products are exact and sums fp32, with the one rounding of out; results do not
  * change from run to run (the order of a sum depends on M, N, K and the GPU). bf16 rows are multiplied as two MXFP8 rows, exact for
- * values down to 2^-14 of the largest of their 32 columns and off by at most 2^-21
+ * values down to 2^-13 of the largest of their 32 columns and off by at most 2^-21
  * of that largest (or 2^-137) below; a sum that passes fp32's range on the way is
  * infinite or NaN. A value of x that is not finite (a byte 0x7F or 0xFF, a
  * code 255) makes its row of out NaN, and no other.

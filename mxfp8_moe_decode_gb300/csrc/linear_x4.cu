@@ -6,8 +6,9 @@
 // fp32. bf16 rows become two MXFP8 rows first: with the group's code c, hi =
 // E4M3(x 2^(127 - c)) and lo = E4M3(16 (x 2^(127 - c) - hi)) under the code c - 4.
 // bf16 has 8 significant bits, hi takes 4 and the rest, at most half a step of
-// hi, fits lo's 4: exact down to 2^-14 of the group's largest value, and off by
-// at most 2^-21 of that below (E4M3's subnormals).
+// hi, fits lo's 4 while x 2^(127 - c) is at least 2^-6, E4M3's smallest normal
+// value: exact down to 2^-13 of the group's largest value, which lies above 224.
+// Below, lo's steps are 2^-13: off by half of one, 2^-21 of the largest, at most.
 //
 // Swap-AB: 128 weight rows are the MMA's M and up to 192 token rows its N, so
 // few tokens still fill the tensor cores' lanes, and the weights stream once

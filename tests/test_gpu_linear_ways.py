@@ -249,3 +249,43 @@ def test_linear_workspaces_side_by_side():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, M.linear_x4(x, w, wc))
+
+
+# ---------------------------------------------------------------- what two parts hold of a bf16 value
+PARTS = [(3, 1100, 1024), (16, 1100, 4096), (13, 40000, 1024), (48, 5120, 5120), (400, 3000, 1024), (72, 4096, 4096),
+         (170, 38913, 640)]
+
+
+@pytest.mark.parametrize("m,n,k", PARTS)
+def test_linear_bf16_values_beside_a_large_one(m, n, k):
+    """Every weight row has a single 1, so a column of out is a column of x as hi and lo hold it: itself from 2^-13 of
+    its group's largest value on, below within 2^-21 of that largest. (Down to 2^-14 is not exact: beside 225, which
+    leaves no scale unused, 225 * 2^-14 lies at 7.03 of hi's steps and its rest at half of lo's last one.)"""
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+    top = torch.exp2(torch.randint(-90, 90, (m, k // 32, 1), generator=g, device=DEV).float())
+    top *= 1 + torch.randint(0, 128, top.shape, generator=g, device=DEV) / 128.0
+    top[0] = 225.0
+    x = torch.randn(m, k // 32, 32, generator=g, device=DEV).sign()
+    x *= top * torch.exp2(-18.0 * torch.rand(x.shape, generator=g, device=DEV))
+    x[:, :, 1] = top[:, :, 0] * 2.0 ** -13
+    x[:, :, 2] = top[:, :, 0] * 2.0 ** -14
+    x[:, :, 3] = -top[:, :, 0] * (2.0 ** -13 * 1.5)
+    x[:, :, 17] = top[:, :, 0]
+    x = x.bfloat16()
+    x = torch.where(x.float().abs() > top, top.bfloat16(), x)  # (rounded past the largest)
+    w = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV)
+    column = (torch.arange(n, device=DEV) * 7 + 1) % k
+    w[torch.arange(n, device=DEV), column // 2] = torch.where(column % 2 == 0, 0x02, 0x20).to(torch.uint8)  # 1.0
+    wc = torch.full((n, k // 32), 127, dtype=torch.uint8, device=DEV)
+    out = M.linear_x4(x.view(m, k), w, wc).double()
+    want, largest = x.view(m, k).double()[:, column], top.expand(-1, -1, 32).reshape(m, k).double()[:, column]
+    exact = want.abs() >= 2.0 ** -13 * largest
+    assert exact.any() and (~exact).any() and torch.equal(out[exact], want[exact])
+    # (below it lo's step is 2^-13 where the largest is above 224: hi + lo has 7 bits at most, out's rounding changes
+    # nothing, and half of that step is below 2^-21 * 224)
+    assert ((out - want).abs() <= 2.0 ** -21 * largest).all()
+
+
+def test_ways_of_the_two_parts():
+    ways = [dict(zip(FIELDS, _way(m, n, k, 0))) for m, n, k in PARTS]
+    assert {(w["products"], w["images"], w["inside"]) for w in ways} >= {(1, 1, 1), (1, 1, 0), (2, 1, 0), (2, 2, 0)}
