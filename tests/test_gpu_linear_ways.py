@@ -7,6 +7,8 @@ linear_x4_shape is asked whether it takes it: where a rule is changed the cases 
 Bounds as tests/test_gpu_layer_limits.py.
 """
 
+import random
+
 import pytest
 import torch
 
@@ -249,6 +251,47 @@ def test_linear_workspaces_side_by_side():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, M.linear_x4(x, w, wc))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_linear_random_shapes(seed):
+    """Shapes over the whole range, three calls at once on three streams, three times each: the same bits, within the
+    bounds, no status."""
+    rng = random.Random(seed)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i in range(60):
+        jobs = []
+        for s in streams:
+            k, n, m = 128 * int(2 ** rng.uniform(0, 7.5)), int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(0, 10.5))
+            mx = rng.random() < 0.5
+            k, n = min(k, 8192) if mx else k, max(1, min(n, int(3e8) // k))
+            m = max(1, min(m, int(1e11) // (n * k)))
+            x, w, wc, xc = _case(m, n, k, mx, seed=i)
+            jobs.append((s, (x, w, wc, xc), torch.zeros(1, dtype=torch.int32, device=DEV), [],
+                         sorted({0, n // 2, rng.randrange(n), n - 1})))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, (x, w, wc, xc), status, outs, _ in jobs:
+                with torch.cuda.stream(s):
+                    outs.append(M.linear_x4(x, w, wc, x_codes=xc, status=status))
+        torch.cuda.synchronize()
+        for _, (x, w, wc, xc), status, outs, columns in jobs:
+            assert status.item() == 0 and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]), (x.shape, w.shape)
+            _check(outs[0], x, w, wc, xc, columns)
+
+
+@pytest.mark.parametrize("m,n,k", [(6, 150, 384), (64, 20000, 1280), (170, 400, 4096), (1295, 1732, 1280)])
+def test_linear_rows_under_a_nan_code(m, n, k):
+    """The code 255 of a row's group makes that row NaN, also where the group's bytes are zeros, and no other row."""
+    x, w, wc, xc = _case(m, n, k, True)
+    want = M.linear_x4(x, w, wc, x_codes=xc)
+    x2, xc2 = x.clone(), xc.clone()
+    xc2[0, 0], xc2[m // 2, k // 32 - 1], xc2[m - 1, 3] = 255, 255, 255
+    x2[m // 2, k - 32:] = 0
+    out = M.linear_x4(x2, w, wc, x_codes=xc2)
+    bad = [0, m // 2, m - 1]
+    rows = [i for i in range(m) if i not in bad]
+    assert torch.isnan(out[bad]).all() and torch.equal(out[rows], want[rows])
 
 
 # ---------------------------------------------------------------- what two parts hold of a bf16 value
