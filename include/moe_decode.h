@@ -523,7 +523,7 @@ typedef struct moe_rope_spec {
  * allocation, no synchronisation, capture safe. head_dim a multiple of 16 in
  * [16, 1024], heads 1..4096. Errors: MOE_ERR_RANGE (tokens < 0 or > 2^24),
  * MOE_ERR_UNSUPPORTED (dims, or more work than a grid holds: tokens * heads *
- * head_dim past 2^42), MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_CUDA. A value that is
+ * head_dim from some 2^45 on), MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_CUDA. A value that is
  * not finite touches its own pair alone.
  */
 int moe_rope(const moe_rope_spec* spec, const void* x, int64_t ldx, int tokens, int heads,
@@ -534,10 +534,11 @@ int moe_rope(const moe_rope_spec* spec, const void* x, int64_t ldx, int tokens, 
  * (the cache's) are turned as moe_rope turns them, q into q_out, k into the
  * cache with v as moe_kv_append_x8 writes them: bit for bit what the two give
  * one after the other. positions int32 [tokens] (device), or null: a token's
- * place in the cache (lens[b] + i). q_out may be q where the strides are equal.
- * Rows of no sequence, and those of a sequence whose length is refused
- * (MOE_KV_STATUS_LENGTH), are left as they were in q_out too; a page id out of
- * range leaves out keys and values only. Strides, limits and errors as
+ * place in the cache (lens[b] + i). q_out may be q where the strides are equal;
+ * it overlaps nothing else. Rows of no sequence, and those of a sequence whose
+ * length is below 0 or above 2^30, are left as they were in q_out too, and where
+ * cu_q falls all are; a page id out of range, and a token beyond the page table,
+ * leave out keys and values only. Strides, limits and errors as
  * moe_kv_append_x8's and moe_rope's; max_q is not read.
  */
 int moe_rope_kv_append_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs,
@@ -612,9 +613,9 @@ int moe_attn_x8(const moe_kv_cache* cache, const moe_kv_seqs* seqs, const void* 
  * code 255) makes its row of out NaN, and no other.
  *
  * workspace: for bf16 rows only (else null will do): device memory, 16-byte
- * aligned, of at least moe_linear_x4_workspace_bytes(M, K, MOE_LINEAR_BF16); it
- * needs no initial state. Calls that may overlap on the GPU, captured ones among
- * them, need workspaces of their own. One kernel on `stream` (bf16 rows: two); no
+ * aligned, of at least moe_linear_x4_workspace_bytes(M, K, MOE_LINEAR_BF16), also
+ * where the call does not touch it (few rows); it needs no initial state. Calls that may overlap on the GPU, captured ones among
+ * them, need workspaces of their own. One kernel on `stream` (bf16 rows: one or two); no
  * allocation, no synchronisation, capture safe. Errors: MOE_ERR_RANGE (M < 0 or >
  * 2^20, N < 0 or > 2^24), MOE_ERR_UNSUPPORTED (K not a multiple of 128 in [128,
  * 65536]), MOE_ERR_ARG (null, a stride below its row, out that is x, a

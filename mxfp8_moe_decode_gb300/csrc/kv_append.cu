@@ -33,7 +33,8 @@
 // 40 query heads of 128 over 8: two prompts of 4100 tokens 38.5 us (214 MB, 5.6
 // TB/s; 32 at the copy's rate, 48 with the queries' CTAs behind the append's),
 // bound by instructions: every key/value head's CTA makes the sines and cosines
-// of its tokens. 48 sequences of one token 4.5 us. By fewer registers 6 or 7 CTAs
+// of its tokens. 48 sequences of one token 4.3 to 4.6 us in
+// graph replays (by single calls from Python 11). By fewer registers 6 or 7 CTAs
 // an SM in place of 5: 38.5 and 38.9, 4 x 128 tokens 9.0 in place of 8.5.
 #include "internal.cuh"
 #include "kv_x8.cuh"

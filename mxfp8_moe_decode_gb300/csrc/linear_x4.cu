@@ -23,17 +23,19 @@
 // its parts in an exchange over distributed shared memory, in the order of the
 // ranks. choose_shape weighs tile heights and shares.
 //
-// What bounds it, and what it takes (calls back to back, weights from HBM):
-//  7 rows, 5120 -> 129281 columns (352 MB): the weights' stream, 56 us (6.3 TB/s)
-//  48 rows, 5120 -> 27648: 18.2 us, of which the stream is 11; the rest is the
+// What bounds it, and what it takes (graph replays of calls back to back, weights
+// from HBM; one by one from Python 0.3 to 0.6 us more):
+//  7 rows, 5120 -> 129281 columns (352 MB): the weights' stream, 55 us (6.4 TB/s)
+//  48 rows, 5120 -> 27648: 18.1 us, of which the stream is 11; the rest is the
 //    start, a CTA's last tile and the exchange
-//  1 row, 5120 -> 7168: 7.7 us. The stream is 2.9; 1.7 are a launch's, 1.1 the
+//  1 row, 5120 -> 7168: 7.6 us. The stream is 2.9; 1.7 are a launch's, 1.1 the
 //    first codes and weights, 1.3 the exchange and the end, and a K block takes
 //    some 100 to 170 ns however few columns it has: one thread issues at most a
 //    block in 300, two half of that, four (a ring of 8 slots) no better
-//  4000 rows, 5120 -> 7168: 102 us, 2880 TFLOP/s; bf16 rows 196 (two products).
-//    The tensor cores work 64 % of the time (two accumulators of 192 columns
-//    fill TMEM, so one thread issues), shared memory 62 %
+//  4000 rows, 5120 -> 7168: 104 us in a short burst (2070 MHz, 2830 TFLOP/s), 112 to
+//    116 in a long run, which the power cap slows (1680 to 1970 MHz, 2530 to 2630);
+//    bf16 rows (two products) 199 and 214. The tensor cores work 64 % of the time (two
+//    accumulators of 192 columns fill TMEM, so one thread issues), shared memory 62 %
 // Slower: weights by plain loads through registers (7 rows above: 133 us) or by
 // cp.async and warps that spread the codes (91 to 107; shared memory's port);
 // pairs of CTAs that share the rows' copies by multicast (no change); tiles of 160
@@ -982,7 +984,7 @@ extern "C" int moe_linear_x4(const void* x, int64_t ldx, const uint8_t* x_codes,
   p.turns = row_turns(shape);
   p.off_b = p.slots * kABytes;
   p.off_img = p.off_b + p.slots * p.slot_b;
-  // (a ring has 3 slots at least, more than the 96 KB that an exchange buffer over it takes)
+  // (a ring has 3 slots at least, more than the 100 KB that an exchange buffer over it takes at most)
   p.off_xchg = shape.over ? 0 : p.off_img + p.slots * p.slot_img;
   p.off_bar = p.off_img + p.slots * p.slot_img + (shape.over ? 0 : shape.xchg);
 

@@ -16,9 +16,10 @@
 // from the loads, all issued before the first use, to the stores: a row is read
 // once, and the two sums cost two exchanges of four floats.
 // 12000 rows of 5120: with a gate per row 91 us (556 MB, 6.1 TB/s, 91 % of a copy's
-// rate), without 73, with normed 88. Arithmetic is in fp32 pairs, and what scales a
-// row is one factor (before: 104 us, bound by instructions). 48 rows 3.3 us: a
-// launch and one row's chain of loads, two exchanges and stores. Six CTAs an SM
+// rate), without 74, with normed beside the gate 107. Arithmetic is in fp32 pairs, and
+// what scales a row is one factor (before: 104 us, bound by instructions). 48 rows 3.0
+// to 3.3 us in graph replays: a launch and one row's chain of loads, two exchanges and
+// stores; by single calls from Python, which allocate three or four outputs, 14 to 16. Six CTAs an SM
 // where a thread has 4 or 5 octets: 93.4 us without (79 registers hold the rows of
 // 5120; of wider ones they would not).
 #include "f32x2.cuh"

@@ -5,8 +5,9 @@
 // Bound by memory, 2 bytes in and 2 out per value. A thread has one item of a
 // head (two 16-byte chunks that hold 8 pairs) and takes the same item of
 // several heads, so its 8 sines and cosines serve all of them (rope::head_groups).
-// 8000 tokens of 40 heads of 128, 64 dims of them in neighbours: 27.0 us (164 MB,
-// 6.1 TB/s, 91 % of a copy's rate); one token 1.7 us, a launch.
+// 8000 tokens of 40 heads of 128, 64 dims of them in neighbours: 26.2 to 27 us (164 MB,
+// 6.1 to 6.3 TB/s, 91 to 94 % of a copy's rate); one token 1.5 us in graph replays, a
+// launch (by single calls from Python 4 to 4.6).
 #include "internal.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
