@@ -36,6 +36,7 @@ WAYS = [
     (331, 396, 3968, 0, (1, 1, 1, 0, 0, 1, 2, 6, 2, 2)),
     (13, 64, 20608, 0, (1, 1, 1, 0, 0, 1, 2, 8, 1, 2)),
     (9, 65, 21504, 0, (1, 1, 1, 0, 0, 1, 2, 8, 2, 2)),
+    (184, 9808, 128, 0, (1, 1, 1, 1, 0, 0, 1, 6, 1, 4)),
     (171, 9750, 256, 0, (1, 1, 1, 1, 0, 0, 1, 6, 2, 4)),
     (1, 64, 1152, 0, (1, 1, 1, 1, 0, 0, 2, 10, 2, 4)),
     (1013, 513, 640, 0, (1, 1, 1, 1, 0, 0, 2, 6, 1, 4)),
